@@ -398,6 +398,87 @@ int32_t lce_ce_logits_fwd_bwd(const lce_tensor *logits, const lce_tensor *target
                               double z_coef, double grad_out, lce_tensor *grad_logits,
                               lce_tensor *workspace, lce_loss *out, void *stream);
 
+/* ---- activation checkpoints in 8 bits ----------------------------------- */
+
+/* A 16-bit activation kept in 8 bits between the forward and the backward:
+ * every 32 consecutive values of a row (the last block of a row may be
+ * shorter) share a power-of-two scale 2^e, e the smallest integer that brings
+ * the block's largest finite magnitude within 448 (at least -117 for bf16 and
+ * -15 for fp16), and each value is stored as the nearest e4m3 number (1 sign,
+ * 4 exponent bits of bias 7, 3 fraction bits; ties to even) to value * 2^-e.
+ * The value read back, code * 2^e, is within 2^-4 of the value relatively, or
+ * within 2^(e-10) for the small values of a block, and is exact in the 16-bit
+ * type (fp16: held at +-65504 where the rounding would pass it).  Infinite
+ * and NaN values read back as NaN and take no part in the block's scale.
+ *   x      [n*d] LCE_BF16 or LCE_F16, row-major [n][d]
+ *   codes  [n*d] LCE_U8
+ *   scales [n*ceil(d/32)] LCE_U8, e + 127
+ * Both calls only enqueue on `stream`.  581/583/584 as
+ * lce_dims_check(n, 1, d), 590 for a dtype, 582 for a short buffer. */
+#define LCE_PACK8_BLOCK 32
+int32_t lce_pack8(const lce_tensor *x, int64_t n, int64_t d, lce_tensor *codes,
+                  lce_tensor *scales, void *stream);
+/* The values a checkpoint stands for, out [n*d] LCE_BF16 or LCE_F16 (the type
+ * it was packed from; another of the two rounds and saturates). */
+int32_t lce_unpack8(const lce_tensor *codes, const lce_tensor *scales, int64_t n, int64_t d,
+                    lce_tensor *out, void *stream);
+
+/* ---- one step of beam search -------------------------------------------- */
+
+/* Bytes of device workspace lce_beam_select needs (-status if refused: 581
+ * for a dimension < 1; 583 for beams > 32, n_out > 64, n_seq > LCE_MAX_N_TOK
+ * or vocab > LCE_MAX_VOCAB; 584 when the rows have 2^24 or more pieces of
+ * 8192 values). */
+int64_t lce_beam_workspace_bytes(int64_t n_seq, int64_t beams, int64_t vocab, int64_t n_out);
+
+/* The n_out best continuations of every sequence: with
+ * total(k, v) = scores[k] + logits[k][v] - lse_k over the allowed tokens v of
+ * beam k (lse_k their log-sum-exp), the n_out largest totals of a sequence's
+ * beams x vocab, best first, equal ones by the lower beam, then the lower
+ * token.  Each beam competes with its n_out largest logits (equal ones by the
+ * lower token); totals are formed and compared in fp64.
+ *   logits       [n_seq*beams*vocab] LCE_BF16, LCE_F16 or LCE_F32
+ *   scores       [n_seq*beams] LCE_F32, the beams' accumulated scores
+ *   finished     [n_seq*beams] LCE_U8 or data == NULL: a beam with nonzero
+ *                offers (eos, scores[k]) alone; its logits are not read
+ *   allowed      [n_seq*beams*vocab] LCE_U8 or data == NULL: tokens with 0
+ *                take no part, whatever their logit
+ *   eos          the end token's id, -1 for none (586 when it is outside
+ *                [-1, vocab), or -1 with finished given)
+ *   out_scores   [n_seq*n_out] LCE_F32, out_parents and out_tokens
+ *                [n_seq*n_out] LCE_I64, out_finished [n_seq*n_out] LCE_U8 or
+ *                NULL (1 where the token is eos)
+ *   workspace    LCE_U8, numel >= lce_beam_workspace_bytes(...)
+ * A beam offers nothing when its score is not finite, when no token with a
+ * logit above -inf is allowed, or when an allowed logit is NaN or +inf.  A
+ * sequence with fewer than n_out candidates ends in entries of score -inf,
+ * parent -1 and token -1.  Only enqueues on `stream`; statuses as
+ * lce_beam_workspace_bytes, 590 for a dtype, 582 for a short buffer. */
+int32_t lce_beam_select(const lce_tensor *logits, const lce_tensor *scores,
+                        const lce_tensor *finished, const lce_tensor *allowed, int64_t n_seq,
+                        int64_t beams, int64_t vocab, int64_t n_out, int64_t eos,
+                        lce_tensor *out_scores, lce_tensor *out_parents, lce_tensor *out_tokens,
+                        lce_tensor *out_finished, lce_tensor *workspace, void *stream);
+
+/* Per-beam states in the order of the parents: for every sequence q and state,
+ * row q*n_out + j of dst = row q*beams + parents[q*n_out + j] of src; a parent
+ * outside [0, beams) gives zeros.  All states have the same geometry: a row
+ * is `segs` segments of `seg_stride` elements, of which the first `seg_elems`
+ * are carried over (a cache [rows][heads][room][d] filled to `length`: segs =
+ * heads, seg_stride = room*d, seg_elems = length*d); what lies behind is
+ * neither read nor written.
+ *   src, dst  arrays of n_states descriptors, any dtypes of one element size;
+ *             src[i].numel >= n_seq*beams*segs*seg_stride and
+ *             dst[i].numel >= n_seq*n_out*segs*seg_stride.  Either every dst
+ *             is its src (in place; needs n_out == beams, and rows that stay
+ *             are not touched) or none overlaps it (582 otherwise)
+ *   parents   [n_seq*n_out] LCE_I64
+ *   beams, n_out  at most 32 (583); the elements of a state at most 2^46 (584)
+ * Only enqueues on `stream`. */
+int32_t lce_beam_reorder(const lce_tensor *src, lce_tensor *dst, int32_t n_states,
+                         const lce_tensor *parents, int64_t n_seq, int64_t beams, int64_t n_out,
+                         int64_t segs, int64_t seg_elems, int64_t seg_stride, void *stream);
+
 /* ---- optional kernel timing (for benchmarks and profilers) ------------- */
 
 /* Kernel kinds a timed call can bracket with events. */

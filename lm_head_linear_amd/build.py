@@ -1,6 +1,6 @@
 """Build liblce.so (HIP for gfx950) in-tree with hipcc.
 
-Every .hip / .cpp source under csrc/ is compiled for gfx950 only and linked
+Every .hip / .cpp source under csrc/ and csrc_ops/ is compiled for gfx950 only and linked
 into lm_head_linear_amd/liblce.so.  Packed-fp32 instructions are disabled
 for all device code.
 """
@@ -13,12 +13,13 @@ import sys
 from concurrent.futures import ThreadPoolExecutor
 
 HERE = os.path.dirname(os.path.abspath(__file__))
-CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(os.path.dirname(HERE), "include")
 LIB = os.path.join(HERE, "liblce.so")
 OBJ_DIR = os.path.join(HERE, "_build")
 
-SOURCES = ["lce_contract.cpp", "lce_ce.hip", "lce_distill.hip"]
+# csrc/ holds the losses, csrc_ops/ the operators that stand next to them.
+SOURCES = ["csrc/lce_contract.cpp", "csrc/lce_ce.hip", "csrc/lce_distill.hip",
+           "csrc_ops/beam.hip", "csrc_ops/checkpoint.hip"]
 
 HIPCC = shutil.which("hipcc") or "/opt/rocm/bin/hipcc"
 ARCH = os.environ.get("LCE_OFFLOAD_ARCH", "gfx950")
@@ -29,8 +30,8 @@ DEVICE = [f"--offload-arch={ARCH}", "-Xclang", "-target-feature", "-Xclang", "-p
 
 
 def _compile(src: str) -> str:
-    path = os.path.join(CSRC, src)
-    obj = os.path.join(OBJ_DIR, src + ".o")
+    path = os.path.join(HERE, src)
+    obj = os.path.join(OBJ_DIR, os.path.basename(src) + ".o")
     if src.endswith(".hip"):
         cmd = [HIPCC, "-x", "hip", *DEVICE, *COMMON, "-c", path, "-o", obj]
     else:

@@ -178,6 +178,17 @@ def lib():
         L.lce_distill_fwd_bwd_timed.argtypes = L.lce_distill_fwd_bwd.argtypes + [PTM]
         L.lce_ce_logits_fwd_bwd_timed.restype = i32
         L.lce_ce_logits_fwd_bwd_timed.argtypes = L.lce_ce_logits_fwd_bwd.argtypes + [PTM]
+        L.lce_pack8.restype = i32
+        L.lce_pack8.argtypes = [PT, i64, i64, PT, PT, vp]
+        L.lce_unpack8.restype = i32
+        L.lce_unpack8.argtypes = [PT, PT, i64, i64, PT, vp]
+        L.lce_beam_workspace_bytes.restype = i64
+        L.lce_beam_workspace_bytes.argtypes = [i64, i64, i64, i64]
+        L.lce_beam_select.restype = i32
+        L.lce_beam_select.argtypes = [PT, PT, PT, PT, i64, i64, i64, i64, i64, PT, PT, PT, PT, PT,
+                                      vp]
+        L.lce_beam_reorder.restype = i32
+        L.lce_beam_reorder.argtypes = [PT, PT, i32, PT, i64, i64, i64, i64, i64, i64, vp]
         _lib = L
     return _lib
 
@@ -514,3 +525,165 @@ def ce_logits(logits, targets, loss_mask=None, z_coef=0.0, grad_out=1.0, want_gr
     if st != OK:
         raise LceError(st, "lce_ce_logits_fwd_bwd")
     return out.as_dict(), g
+
+
+# ------------------------------------------- operators next to the losses
+
+def _on(*tensors) -> torch.device:
+    """The one GPU that all given tensors are on; ValueError otherwise."""
+    dev = None
+    for x in tensors:
+        if x is None:
+            continue
+        if not x.is_cuda:
+            raise ValueError("tensors must be on a GPU")
+        if dev is None:
+            dev = x.device
+        elif x.device != dev:
+            raise ValueError("tensors must be on one device")
+    return dev
+
+
+def _check(st: int, where: str):
+    if st != OK:
+        raise LceError(st, where)
+
+
+def lce_pack8(x, n, d, codes, scales, stream: Optional[int] = None) -> int:
+    """Direct call of the C entry point; returns the status."""
+    a, c, s = _t(x), _t(codes), _t(scales)
+    return lib().lce_pack8(ctypes.byref(a), n, d, ctypes.byref(c), ctypes.byref(s),
+                           stream if stream is not None else _stream(x.device))
+
+
+def lce_unpack8(codes, scales, n, d, out, stream: Optional[int] = None) -> int:
+    """Direct call of the C entry point; returns the status."""
+    c, s, o = _t(codes), _t(scales), _t(out)
+    return lib().lce_unpack8(ctypes.byref(c), ctypes.byref(s), n, d, ctypes.byref(o),
+                             stream if stream is not None else _stream(codes.device))
+
+
+PACK8_BLOCK = 32
+
+
+@dataclass
+class Packed8:
+    """A 16-bit activation [n][d] kept in 8 bits: e4m3 codes [n][d] and the
+    biased exponents [n][ceil(d / 32)] of the blocks' power-of-two scales;
+    dtype is the type it came from."""
+    codes: torch.Tensor
+    scales: torch.Tensor
+    dtype: torch.dtype
+
+
+def pack8(x) -> Packed8:
+    """Allocate codes and scales, call lce_pack8."""
+    n, d = x.shape
+    with torch.cuda.device(_on(x)):
+        codes = torch.empty(n, d, dtype=torch.uint8, device=x.device)
+        scales = torch.empty(n, -(-d // PACK8_BLOCK), dtype=torch.uint8, device=x.device)
+        _check(lce_pack8(x, n, d, codes, scales), "lce_pack8")
+    return Packed8(codes, scales, x.dtype)
+
+
+def unpack8(packed: Packed8):
+    """Allocate the 16-bit tensor, call lce_unpack8."""
+    n, d = packed.codes.shape
+    with torch.cuda.device(_on(packed.codes, packed.scales)):
+        out = torch.empty(n, d, dtype=packed.dtype, device=packed.codes.device)
+        _check(lce_unpack8(packed.codes, packed.scales, n, d, out), "lce_unpack8")
+    return out
+
+
+def lce_beam_workspace_bytes(n_seq: int, beams: int, vocab: int, n_out: int) -> int:
+    return lib().lce_beam_workspace_bytes(n_seq, beams, vocab, n_out)
+
+
+def lce_beam_select(logits, scores, finished, allowed, n_seq, beams, vocab, n_out, eos,
+                    out_scores, out_parents, out_tokens, out_finished, workspace,
+                    stream: Optional[int] = None) -> int:
+    """Direct call of the C entry point; returns the status."""
+    ts = [_t(x) for x in (logits, scores, finished, allowed)]
+    os_ = [_t(x) for x in (out_scores, out_parents, out_tokens, out_finished, workspace)]
+    return lib().lce_beam_select(*[ctypes.byref(a) for a in ts], n_seq, beams, vocab, n_out, eos,
+                                 *[ctypes.byref(a) for a in os_],
+                                 stream if stream is not None else _stream(logits.device))
+
+
+def lce_beam_reorder(src, dst, parents, n_seq, beams, n_out, segs, seg_elems, seg_stride,
+                     stream: Optional[int] = None) -> int:
+    """Direct call of the C entry point for lists of states; returns the status."""
+    n = len(src)
+    if len(dst) != n:
+        raise ValueError("as many destinations as sources are needed")
+    a, b = (Tensor * n)(*[_t(x) for x in src]), (Tensor * n)(*[_t(x) for x in dst])
+    p = _t(parents)
+    return lib().lce_beam_reorder(a, b, n, ctypes.byref(p), n_seq, beams, n_out, segs, seg_elems,
+                                  seg_stride,
+                                  stream if stream is not None else _stream(parents.device))
+
+
+@dataclass
+class BeamStep:
+    """What a beam step chose, best first: scores fp32, parents and tokens
+    int64, finished bool, all [n_seq][n_out]."""
+    scores: torch.Tensor
+    parents: torch.Tensor
+    tokens: torch.Tensor
+    finished: torch.Tensor
+
+
+def beam_select(logits, scores, n_out, finished=None, allowed=None, eos=None, workspace=None):
+    """Allocate the outputs and (if needed) the workspace, call lce_beam_select
+    for logits [n_seq*beams][vocab] and scores [n_seq][beams]."""
+    n_seq, beams = scores.shape
+    rows, V = logits.shape
+    if rows != n_seq * beams:
+        raise ValueError("logits need one row per beam")
+    dev = _on(logits, scores, finished, allowed, workspace)
+    with torch.cuda.device(dev):
+        nbytes = lce_beam_workspace_bytes(n_seq, beams, V, n_out)
+        if nbytes < 0:
+            raise LceError(int(-nbytes), "lce_beam_workspace_bytes")
+        ws = workspace if workspace is not None else torch.empty(nbytes, dtype=torch.uint8,
+                                                                 device=dev)
+        step = BeamStep(torch.empty(n_seq, n_out, dtype=torch.float32, device=dev),
+                        torch.empty(n_seq, n_out, dtype=torch.int64, device=dev),
+                        torch.empty(n_seq, n_out, dtype=torch.int64, device=dev),
+                        torch.empty(n_seq, n_out, dtype=torch.bool, device=dev))
+        _check(lce_beam_select(logits, scores, finished, allowed, n_seq, beams, V, n_out,
+                               -1 if eos is None else int(eos), step.scores, step.parents,
+                               step.tokens, step.finished, ws), "lce_beam_select")
+    return step
+
+
+def beam_reorder(states, parents, beams, out=None, length=None, dim=2):
+    """Rows of every state [n_seq*beams][...] in the order of parents
+    [n_seq][n_out], by lce_beam_reorder: into `out` (a list of tensors
+    [n_seq*n_out][...]), or in place without it.  `length` carries over the
+    first `length` entries of dimension `dim` only.  Returns the list written."""
+    out = states if out is None else out
+    n_seq, n_out = parents.shape
+    shape = states[0].shape[1:]
+    for x, y in zip(states, out):
+        if (x.shape[0] != n_seq * beams or y.shape[0] != n_seq * n_out or x.shape[1:] != shape
+                or y.shape[1:] != shape):
+            raise ValueError("states need one shape and one row per beam")
+    size = 1
+    for s in shape:
+        size *= s
+    if length is None:
+        segs, elems, stride = 1, size, size
+    else:
+        if not (1 <= dim <= len(shape) and 0 <= length <= shape[dim - 1]):
+            raise ValueError("length is outside the dimension")
+        segs, inner = 1, 1
+        for s in shape[:dim - 1]:
+            segs *= s
+        for s in shape[dim:]:
+            inner *= s
+        elems, stride = length * inner, shape[dim - 1] * inner
+    with torch.cuda.device(_on(parents, *states, *out)):
+        _check(lce_beam_reorder(states, out, parents, n_seq, beams, n_out, segs, elems, stride),
+               "lce_beam_reorder")
+    return out

@@ -1,0 +1,112 @@
+"""Refusals of the operators next to the losses: decided on the host before
+any device call, so they are checked without a GPU (CPU buffers)."""
+import pytest
+import torch
+
+from lm_head_linear_amd import lce
+
+U8 = torch.uint8
+
+
+def test_checkpoint_refusals():
+    x = torch.zeros(4, 40, dtype=torch.bfloat16)
+    codes, scales = torch.zeros(4, 40, dtype=U8), torch.zeros(4, 2, dtype=U8)
+    call = lambda **kw: lce.lce_pack8(**{**dict(x=x, n=4, d=40, codes=codes, scales=scales,
+                                                stream=0), **kw})
+    back = lambda **kw: lce.lce_unpack8(**{**dict(codes=codes, scales=scales, n=4, d=40, out=x,
+                                                  stream=0), **kw})
+    for f in (call, back):
+        assert f(n=0) == 581
+        assert f(d=0) == 581
+        assert f(d=-3) == 581
+        assert f(n=2 ** 24 + 1) == 583
+        assert f(d=2 ** 24 + 1) == 583
+        assert f(n=2 ** 24, d=2 ** 23) == 584
+        assert f(codes=codes.int()) == 590
+        assert f(scales=scales.float()) == 590
+        assert f(codes=codes[:3]) == 582
+        assert f(scales=scales[:, :1].contiguous()) == 582
+    assert call(x=x.float()) == 590
+    assert back(out=x.float()) == 590
+    assert call(x=x[:3]) == 582
+    assert back(out=x[:3]) == 582
+    with pytest.raises(ValueError):
+        lce.pack8(x)                                    # not on a GPU
+
+
+def test_beam_select_refusals():
+    n_seq, beams, V, n_out = 2, 3, 50, 4
+    rows = n_seq * beams
+    ws = lce.lce_beam_workspace_bytes(n_seq, beams, V, n_out)
+    assert ws > 0
+    w = lce.lce_beam_workspace_bytes
+    assert w(0, 3, 50, 4) == -581 and w(2, 0, 50, 4) == -581
+    assert w(2, 3, 0, 4) == -581 and w(2, 3, 50, 0) == -581
+    assert w(2, 33, 50, 4) == -583 and w(2, 3, 50, 65) == -583
+    assert w(2 ** 24 + 1, 3, 50, 4) == -583 and w(2, 3, 2 ** 24 + 1, 4) == -583
+    assert w(2 ** 20, 32, 50, 4) == -584
+    base = dict(logits=torch.zeros(rows, V), scores=torch.zeros(rows), finished=None, allowed=None,
+                n_seq=n_seq, beams=beams, vocab=V, n_out=n_out, eos=-1,
+                out_scores=torch.zeros(n_seq * n_out),
+                out_parents=torch.zeros(n_seq * n_out, dtype=torch.int64),
+                out_tokens=torch.zeros(n_seq * n_out, dtype=torch.int64), out_finished=None,
+                workspace=torch.zeros(ws, dtype=U8), stream=0)
+    call = lambda **kw: lce.lce_beam_select(**{**base, **kw})
+    assert call(n_seq=0) == 581
+    assert call(beams=33) == 583
+    assert call(n_out=65) == 583
+    assert call(logits=torch.zeros(rows, V, dtype=torch.float64)) == 590
+    assert call(scores=torch.zeros(rows, dtype=torch.float16)) == 590
+    assert call(out_tokens=torch.zeros(n_seq * n_out, dtype=torch.int32)) == 590
+    assert call(finished=torch.zeros(rows), eos=1) == 590
+    assert call(allowed=torch.zeros(rows, V)) == 590
+    assert call(out_finished=torch.zeros(n_seq * n_out)) == 590
+    assert call(workspace=torch.zeros(ws)) == 590
+    assert call(logits=torch.zeros(rows, V - 1)) == 582
+    assert call(scores=torch.zeros(rows - 1)) == 582
+    assert call(out_parents=torch.zeros(n_seq * n_out - 1, dtype=torch.int64)) == 582
+    assert call(finished=torch.zeros(rows - 1, dtype=U8), eos=1) == 582
+    assert call(allowed=torch.zeros(rows, V - 1, dtype=U8)) == 582
+    assert call(out_finished=torch.zeros(n_seq * n_out - 1, dtype=U8)) == 582
+    assert call(workspace=torch.zeros(ws - 1, dtype=U8)) == 582
+    assert call(eos=V) == 586
+    assert call(eos=-2) == 586
+    assert call(finished=torch.zeros(rows, dtype=U8)) == 586
+    with pytest.raises(ValueError):
+        lce.beam_select(torch.zeros(rows, V), torch.zeros(n_seq, beams), 4)
+    with pytest.raises(ValueError):
+        lce.beam_select(torch.zeros(rows + 1, V), torch.zeros(n_seq, beams), 4)
+
+
+def test_beam_reorder_refusals():
+    n_seq, beams = 2, 3
+    src, dst = [torch.zeros(6, 20)], [torch.zeros(6, 20)]
+    p = torch.zeros(n_seq, beams, dtype=torch.int64)
+    base = dict(src=src, dst=dst, parents=p, n_seq=n_seq, beams=beams, n_out=beams, segs=4,
+                seg_elems=5, seg_stride=5, stream=0)
+    call = lambda **kw: lce.lce_beam_reorder(**{**base, **kw})
+    assert call(src=[], dst=[]) == 581
+    for k in ("n_seq", "beams", "n_out", "segs", "seg_stride"):
+        assert call(**{k: 0}) == 581
+    assert call(seg_elems=-1) == 581
+    assert call(beams=33) == 583
+    assert call(n_out=33) == 583
+    assert call(n_seq=2 ** 24 + 1) == 583
+    assert call(segs=2 ** 40, seg_stride=2 ** 10) == 584
+    assert call(parents=p.int()) == 590
+    assert call(dst=[torch.zeros(6, 20, dtype=torch.int64)]) == 590
+    assert call(src=src * 2, dst=dst + [torch.zeros(6, 20, dtype=torch.float16)]) == 590
+    assert call(seg_elems=6) == 582
+    assert call(parents=p[:1]) == 582
+    assert call(src=[torch.zeros(5, 20)]) == 582
+    assert call(dst=[torch.zeros(5, 20)]) == 582
+    # an overlap, some in place and some not, in place with another row count
+    room = torch.zeros(7, 20)
+    assert call(src=[room[:6]], dst=[room[1:]]) == 582
+    assert call(src=[src[0], room[:6]], dst=[src[0], torch.zeros(6, 20)]) == 582
+    assert call(src=[room[:6]], dst=[room[:6]], n_out=2, parents=p) == 582
+    assert call(seg_elems=0) == 580                     # nothing to carry over
+    with pytest.raises(ValueError):
+        lce.beam_reorder(src, p, beams)
+    with pytest.raises(ValueError):
+        lce.lce_beam_reorder(src, dst * 2, p, 2, 3, 3, 4, 5, 5, 0)
