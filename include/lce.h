@@ -398,6 +398,63 @@ int32_t lce_ce_logits_fwd_bwd(const lce_tensor *logits, const lce_tensor *target
                               double z_coef, double grad_out, lce_tensor *grad_logits,
                               lce_tensor *workspace, lce_loss *out, void *stream);
 
+/* ---- linear layer: the product with bias, activation and residual -------- */
+
+#define LCE_ACT_NONE 0
+#define LCE_ACT_RELU 1
+#define LCE_ACT_GELU 2 /* z/2 (1 + erf(z / sqrt 2)) */
+#define LCE_ACT_SILU 3 /* z / (1 + exp(-z))         */
+
+/* Bytes of device workspace lce_linear and lce_linear_backward need
+ * (-status if refused: lce_dims_check(n_tok, d_in, d_out), then 590 unless
+ * dtype is LCE_BF16 or LCE_F16). */
+int64_t lce_linear_workspace_bytes(int64_t n_tok, int64_t d_in, int64_t d_out, int32_t dtype);
+int64_t lce_linear_backward_workspace_bytes(int64_t n_tok, int64_t d_in, int64_t d_out,
+                                            int32_t dtype);
+
+/* out = act(z) + residual, z = x weight^T + bias: the layer in front of a
+ * head, or the head's logits themselves.
+ *   x        [n_tok*d_in] LCE_BF16 or LCE_F16, row-major [n_tok][d_in]
+ *   weight   [d_out*d_in] same dtype, row-major [d_out][d_in]
+ *   bias     [d_out] x's dtype or LCE_F32, or data == NULL
+ *   residual [n_tok*d_out] x's dtype, or data == NULL; may be out itself
+ *   activation LCE_ACT_* (else 588)
+ *   preact   [n_tok*d_out] x's dtype, receives z for the backward, or
+ *            data == NULL
+ *   out      [n_tok*d_out] x's dtype or LCE_F32
+ *   workspace LCE_U8, numel >= lce_linear_workspace_bytes(...)
+ * Products are summed in fp32; bias, activation and residual are applied to
+ * the fp32 sum, and out and preact are each rounded once.  The sums run in a
+ * fixed order: the same call gives the same bits.  Only enqueues on
+ * `stream`.  Statuses as the workspace query, 582 for a short buffer. */
+int32_t lce_linear(const lce_tensor *x, const lce_tensor *weight, const lce_tensor *bias,
+                   const lce_tensor *residual, int64_t n_tok, int64_t d_in, int64_t d_out,
+                   int32_t activation, lce_tensor *preact, lce_tensor *out, lce_tensor *workspace,
+                   void *stream);
+
+/* Gradients of lce_linear: with g = d_out_grad * act'(z),
+ *   d_x = g weight,  d_weight (+)= g^T x,  d_bias (+)= sum over tokens of g
+ * (the residual's gradient is d_out_grad itself).
+ *   d_out_grad [n_tok*d_out] LCE_BF16 or LCE_F16
+ *   x          [n_tok*d_in] the same dtype, or the codes (LCE_U8) of an 8-bit
+ *              checkpoint with its scales in x_scales; only read for d_weight
+ *   weight     [d_out*d_in] the same dtype; only read for d_x
+ *   preact     [n_tok*d_out] z as lce_linear stored it, or its checkpoint's
+ *              codes with preact_scales; ignored with LCE_ACT_NONE
+ *   d_x        [n_tok*d_in] d_out_grad's dtype; d_weight [d_out*d_in] and
+ *              d_bias [d_out] that dtype or LCE_F32; each may be NULL or have
+ *              data == NULL (not all three)
+ *   accumulate nonzero: d_weight and d_bias are added to, else overwritten
+ *   workspace  LCE_U8, numel >= lce_linear_backward_workspace_bytes(...)
+ * g is rounded to the 16-bit type once for the products (not for d_bias).
+ * Outputs must not overlap inputs.  Only enqueues on `stream`. */
+int32_t lce_linear_backward(const lce_tensor *d_out_grad, const lce_tensor *x,
+                            const lce_tensor *x_scales, const lce_tensor *weight,
+                            const lce_tensor *preact, const lce_tensor *preact_scales,
+                            int64_t n_tok, int64_t d_in, int64_t d_out, int32_t activation,
+                            lce_tensor *d_x, lce_tensor *d_weight, lce_tensor *d_bias,
+                            int32_t accumulate, lce_tensor *workspace, void *stream);
+
 /* ---- activation checkpoints in 8 bits ----------------------------------- */
 
 /* A 16-bit activation kept in 8 bits between the forward and the backward:

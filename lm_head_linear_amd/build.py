@@ -19,7 +19,7 @@ OBJ_DIR = os.path.join(HERE, "_build")
 
 # csrc/ holds the losses, csrc_ops/ the operators that stand next to them.
 SOURCES = ["csrc/lce_contract.cpp", "csrc/lce_ce.hip", "csrc/lce_distill.hip",
-           "csrc_ops/beam.hip", "csrc_ops/checkpoint.hip"]
+           "csrc_ops/beam.hip", "csrc_ops/checkpoint.hip", "csrc_ops/linear.hip"]
 
 HIPCC = shutil.which("hipcc") or "/opt/rocm/bin/hipcc"
 ARCH = os.environ.get("LCE_OFFLOAD_ARCH", "gfx950")

@@ -189,6 +189,15 @@ def lib():
                                       vp]
         L.lce_beam_reorder.restype = i32
         L.lce_beam_reorder.argtypes = [PT, PT, i32, PT, i64, i64, i64, i64, i64, i64, vp]
+        L.lce_linear_workspace_bytes.restype = i64
+        L.lce_linear_workspace_bytes.argtypes = [i64, i64, i64, i32]
+        L.lce_linear_backward_workspace_bytes.restype = i64
+        L.lce_linear_backward_workspace_bytes.argtypes = [i64, i64, i64, i32]
+        L.lce_linear.restype = i32
+        L.lce_linear.argtypes = [PT, PT, PT, PT, i64, i64, i64, i32, PT, PT, PT, vp]
+        L.lce_linear_backward.restype = i32
+        L.lce_linear_backward.argtypes = [PT, PT, PT, PT, PT, PT, i64, i64, i64, i32, PT, PT, PT,
+                                          i32, PT, vp]
         _lib = L
     return _lib
 
@@ -687,3 +696,115 @@ def beam_reorder(states, parents, beams, out=None, length=None, dim=2):
         _check(lce_beam_reorder(states, out, parents, n_seq, beams, n_out, segs, elems, stride),
                "lce_beam_reorder")
     return out
+
+
+ACTIVATIONS = {"none": 0, "relu": 1, "gelu": 2, "silu": 3}
+
+
+def lce_linear_workspace_bytes(n_tok: int, d_in: int, d_out: int, dtype) -> int:
+    dt = _DT[dtype] if isinstance(dtype, torch.dtype) else int(dtype)
+    return lib().lce_linear_workspace_bytes(n_tok, d_in, d_out, dt)
+
+
+def lce_linear_backward_workspace_bytes(n_tok: int, d_in: int, d_out: int, dtype) -> int:
+    dt = _DT[dtype] if isinstance(dtype, torch.dtype) else int(dtype)
+    return lib().lce_linear_backward_workspace_bytes(n_tok, d_in, d_out, dt)
+
+
+def lce_linear(x, weight, bias, residual, n_tok, d_in, d_out, activation, preact, out, workspace,
+               stream: Optional[int] = None) -> int:
+    """Direct call of the C entry point; returns the status."""
+    ts = [_t(a) for a in (x, weight, bias, residual)]
+    os_ = [_t(a) for a in (preact, out, workspace)]
+    return lib().lce_linear(*[ctypes.byref(a) for a in ts], n_tok, d_in, d_out, activation,
+                            *[ctypes.byref(a) for a in os_],
+                            stream if stream is not None else _stream(x.device))
+
+
+def lce_linear_backward(d_out_grad, x, x_scales, weight, preact, preact_scales, n_tok, d_in, d_out,
+                        activation, d_x, d_weight, d_bias, accumulate, workspace,
+                        stream: Optional[int] = None) -> int:
+    """Direct call of the C entry point; returns the status."""
+    ts = [_t(a) for a in (d_out_grad, x, x_scales, weight, preact, preact_scales)]
+    os_ = [_t(a) for a in (d_x, d_weight, d_bias)]
+    ws = _t(workspace)
+    return lib().lce_linear_backward(*[ctypes.byref(a) for a in ts], n_tok, d_in, d_out,
+                                     activation, *[ctypes.byref(a) for a in os_], int(accumulate),
+                                     ctypes.byref(ws),
+                                     stream if stream is not None else _stream(d_out_grad.device))
+
+
+@dataclass
+class LinearResult:
+    """out [n][d_out], and z = x weight^T + bias (preact) if it was asked for."""
+    out: torch.Tensor
+    preact: Optional[torch.Tensor]
+
+
+@dataclass
+class LinearGrads:
+    d_x: Optional[torch.Tensor]
+    d_weight: Optional[torch.Tensor]
+    d_bias: Optional[torch.Tensor]
+
+
+def linear(x, weight, bias=None, residual=None, activation="none", want_preact=False,
+           out_dtype=None, workspace=None) -> LinearResult:
+    """act(x weight^T + bias) + residual: allocate out, preact (if wanted) and
+    (if needed) the workspace, call lce_linear."""
+    n, d_in = x.shape
+    d_out = weight.shape[0]
+    if weight.shape[1] != d_in or (bias is not None and bias.numel() != d_out) or (
+            residual is not None and residual.shape != (n, d_out)):
+        raise ValueError("weight, bias or residual does not fit x")
+    dev = _on(x, weight, bias, residual, workspace)
+    with torch.cuda.device(dev):
+        if workspace is None:
+            nbytes = lce_linear_workspace_bytes(n, d_in, d_out, x.dtype)
+            if nbytes < 0:
+                raise LceError(int(-nbytes), "lce_linear_workspace_bytes")
+            workspace = torch.empty(nbytes, dtype=torch.uint8, device=dev)
+        out = torch.empty(n, d_out, dtype=out_dtype or x.dtype, device=dev)
+        preact = torch.empty(n, d_out, dtype=x.dtype, device=dev) if want_preact else None
+        _check(lce_linear(x, weight, bias, residual, n, d_in, d_out,
+                          ACTIVATIONS.get(activation, -1), preact, out, workspace), "lce_linear")
+    return LinearResult(out, preact)
+
+
+def linear_backward(d_out, x, weight, preact=None, activation="none", want_x=True,
+                    want_weight=True, want_bias=False, weight_grad_dtype=None, d_weight=None,
+                    d_bias=None, accumulate=False, workspace=None) -> LinearGrads:
+    """Gradients of linear(): allocate those wanted (d_weight in
+    weight_grad_dtype, fp32 unless given, d_bias in fp32) and (if needed) the
+    workspace, call lce_linear_backward.  x and preact may each be a Packed8;
+    x may be None without want_weight, weight without want_x.  d_weight and
+    d_bias may be given, and are added to with accumulate."""
+    n, m = d_out.shape
+    xs = zs = None
+    if isinstance(x, Packed8):
+        x, xs = x.codes, x.scales
+    if isinstance(preact, Packed8):
+        preact, zs = preact.codes, preact.scales
+    d_in = weight.shape[1] if weight is not None else x.shape[1]
+    if (x is not None and x.shape != (n, d_in)) or (weight is not None and weight.shape[0] != m):
+        raise ValueError("x or weight does not fit d_out")
+    if accumulate and ((want_weight and d_weight is None) or (want_bias and d_bias is None)):
+        raise ValueError("accumulate needs the gradients it adds to")
+    dev = _on(d_out, x, xs, weight, preact, zs, d_weight, d_bias, workspace)
+    with torch.cuda.device(dev):
+        if workspace is None:
+            nbytes = lce_linear_backward_workspace_bytes(n, d_in, m, d_out.dtype)
+            if nbytes < 0:
+                raise LceError(int(-nbytes), "lce_linear_backward_workspace_bytes")
+            workspace = torch.empty(nbytes, dtype=torch.uint8, device=dev)
+        d_x = torch.empty(n, d_in, dtype=d_out.dtype, device=dev) if want_x else None
+        if want_weight and d_weight is None:
+            d_weight = torch.empty(m, d_in, dtype=weight_grad_dtype or torch.float32, device=dev)
+        if want_bias and d_bias is None:
+            d_bias = torch.empty(m, dtype=torch.float32, device=dev)
+        _check(lce_linear_backward(d_out, x, xs, weight, preact, zs, n, d_in, m,
+                                   ACTIVATIONS.get(activation, -1), d_x,
+                                   d_weight if want_weight else None,
+                                   d_bias if want_bias else None, accumulate, workspace),
+               "lce_linear_backward")
+    return LinearGrads(d_x, d_weight, d_bias)

@@ -110,3 +110,69 @@ def test_beam_reorder_refusals():
         lce.beam_reorder(src, p, beams)
     with pytest.raises(ValueError):
         lce.lce_beam_reorder(src, dst * 2, p, 2, 3, 3, 4, 5, 5, 0)
+
+
+def test_linear_refusals():
+    n, d_in, d_out = 3, 10, 12
+    t = torch.bfloat16
+    w = lce.lce_linear_workspace_bytes
+    v = lce.lce_linear_backward_workspace_bytes
+    for f in (w, v):
+        assert f(n, d_in, d_out, t) > 0 and f(n, d_in, d_out, torch.float16) > 0
+        assert f(0, d_in, d_out, t) == -581 and f(n, 0, d_out, t) == -581
+        assert f(n, d_in, 0, t) == -581
+        assert f(n, 2 ** 16 + 1, d_out, t) == -583 and f(2 ** 24, 2 ** 12, 2 ** 12, t) == -584
+        assert f(n, d_in, d_out, torch.float32) == -590
+    base = dict(x=torch.zeros(n, d_in, dtype=t), weight=torch.zeros(d_out, d_in, dtype=t),
+                bias=torch.zeros(d_out), residual=torch.zeros(n, d_out, dtype=t), n_tok=n,
+                d_in=d_in, d_out=d_out, activation=2, preact=torch.zeros(n, d_out, dtype=t),
+                out=torch.zeros(n, d_out, dtype=t),
+                workspace=torch.zeros(w(n, d_in, d_out, t), dtype=U8), stream=0)
+    call = lambda **kw: lce.lce_linear(**{**base, **kw})
+    assert call(n_tok=0) == 581 and call(d_in=0) == 581 and call(d_out=-1) == 581
+    assert call(d_in=2 ** 16 + 1) == 583
+    assert call(n_tok=2 ** 24, d_in=2 ** 12, d_out=2 ** 12) == 584
+    assert call(x=base["x"].float()) == 590
+    for k in ("weight", "residual", "preact", "out"):
+        assert call(**{k: base[k].half()}) == 590, k
+    assert call(bias=torch.zeros(d_out, dtype=torch.float64)) == 590
+    assert call(workspace=base["workspace"].float()) == 590
+    for k in ("x", "weight", "bias", "residual", "preact", "out", "workspace"):
+        assert call(**{k: base[k][:-1]}) == 582, k
+    assert call(x=None) in (582, 590)
+    assert call(out=None) in (582, 590)
+    assert call(activation=4) == 588 and call(activation=-1) == 588
+    with pytest.raises(ValueError):
+        lce.linear(base["x"], base["weight"])               # not on a GPU
+    with pytest.raises(ValueError):
+        lce.linear(base["x"], base["weight"][:, :9])
+
+    bw = dict(d_out_grad=torch.zeros(n, d_out, dtype=t), x=base["x"], x_scales=None,
+              weight=base["weight"], preact=base["preact"], preact_scales=None, n_tok=n, d_in=d_in,
+              d_out=d_out, activation=2, d_x=torch.zeros(n, d_in, dtype=t),
+              d_weight=torch.zeros(d_out, d_in), d_bias=torch.zeros(d_out), accumulate=0,
+              workspace=torch.zeros(v(n, d_in, d_out, t), dtype=U8), stream=0)
+    call = lambda **kw: lce.lce_linear_backward(**{**bw, **kw})
+    codes, zcodes = torch.zeros(n, d_in, dtype=U8), torch.zeros(n, d_out, dtype=U8)
+    scales, zscales = torch.zeros(n, 1, dtype=U8), torch.zeros(n, 1, dtype=U8)
+    assert call(n_tok=0) == 581 and call(d_in=0) == 581 and call(d_out=0) == 581
+    assert call(d_in=2 ** 16 + 1) == 583
+    assert call(d_x=None, d_weight=None, d_bias=None) == 582
+    assert call(weight=None) == 582 and call(x=None) == 582 and call(preact=None) == 582
+    assert call(d_out_grad=bw["d_out_grad"].float()) == 590
+    for k in ("x", "weight", "preact", "d_x", "d_weight", "d_bias"):
+        assert call(**{k: bw[k].half()}) == 590, k
+    assert call(x=codes) == 590 and call(x_scales=scales) == 590
+    assert call(x=codes, x_scales=scales.float()) == 590
+    assert call(preact=zcodes) == 590 and call(preact_scales=zscales) == 590
+    assert call(x=codes, x_scales=scales[:2]) == 582
+    assert call(preact=zcodes, preact_scales=zscales[:2]) == 582
+    for k in ("d_out_grad", "x", "weight", "preact", "d_x", "d_weight", "d_bias", "workspace"):
+        assert call(**{k: bw[k][:-1]}) == 582, k
+    assert call(activation=7) == 588
+    with pytest.raises(ValueError):
+        lce.linear_backward(bw["d_out_grad"], base["x"], base["weight"], base["preact"])
+    with pytest.raises(ValueError):
+        lce.linear_backward(bw["d_out_grad"], base["x"], base["weight"][:5], base["preact"])
+    with pytest.raises(ValueError):
+        lce.linear_backward(bw["d_out_grad"], base["x"], base["weight"], accumulate=True)
