@@ -422,7 +422,8 @@ int64_t lce_linear_backward_workspace_bytes(int64_t n_tok, int64_t d_in, int64_t
  *   preact   [n_tok*d_out] x's dtype, receives z for the backward, or
  *            data == NULL
  *   out      [n_tok*d_out] x's dtype or LCE_F32
- *   workspace LCE_U8, numel >= lce_linear_workspace_bytes(...)
+ *   workspace LCE_U8, numel >= lce_linear_workspace_bytes(...); may be NULL
+ *            where that is 0
  * Products are summed in fp32; bias, activation and residual are applied to
  * the fp32 sum, and out and preact are each rounded once.  The sums run in a
  * fixed order: the same call gives the same bits.  Only enqueues on

@@ -9,137 +9,262 @@
 //   d_weight  dW[o][i]  : m = i (X, MN-major), c = o (G, MN-major), depth n
 // with G = dY * act'(Z), rounded to the 16-bit type once (it feeds matrix
 // instructions); the bias gradient sums the unrounded G in fp32.
+//
+// Up to 64 tokens run in few_tokens_kernel, which is bound by the read of W;
+// more run on tiles in LDS: the 256 x 256 core of the losses where its tiles
+// fill the chip, else 128 x 128 or 64 x 64 tiles, with the depth split over
+// several tiles where there are few (plan_product).
 #include <math.h>
 
-#include "ops_common.h"
+#include "ops_gemm.hpp"
 
 namespace lce {
 
-enum Act { kNone = LCE_ACT_NONE, kRelu = LCE_ACT_RELU, kGelu = LCE_ACT_GELU, kSilu = LCE_ACT_SILU };
+// ------------------------------------------------------------- few tokens --
 
-__device__ inline float act_value(float z, int act) {
-  switch (act) {
-    case kRelu: return z > 0.0f || z != z ? z : 0.0f;
-    case kGelu: return 0.5f * z * (1.0f + erff(z * 0.70710678118654752f));
-    case kSilu: return z / (1.0f + __expf(-z));
-    default: return z;
-  }
+// Up to 64 tokens: the read of W bounds the call, so W goes straight from
+// memory to the registers that feed the matrix instruction.  A wave owns 16
+// rows of W and all tokens (16 T of them): per 32 k one 16-byte load a lane
+// of W and T of X (the block's waves share X, which stays in L1), and T
+// 16x16x32 products.  The loads of the next 128 k are in flight while the
+// current ones are used.  Where d_out is small, KW waves of a block share 16
+// rows, each a range of k, and their sums meet in LDS.  No alignment is asked
+// for: vector loads take any address.
+typedef float f32x4v __attribute__((ext_vector_type(4)));
+template <bool F16>
+__device__ inline f32x4v mfma16(u32x4 a, u32x4 b, f32x4v c) {
+  if constexpr (F16)
+    return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, a),
+                                                  __builtin_bit_cast(f16x8, b), c, 0, 0, 0);
+  else
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a),
+                                                   __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
 }
-__device__ inline float act_slope(float z, int act) {
-  switch (act) {
-    case kRelu: return z > 0.0f ? 1.0f : 0.0f;
-    case kGelu:
-      return 0.5f * (1.0f + erff(z * 0.70710678118654752f)) +
-             z * 0.39894228040143268f * __expf(-0.5f * z * z);
-    case kSilu: {
-      const float s = 1.0f / (1.0f + __expf(-z));
-      return s * (1.0f + z * (1.0f - s));
+
+// Eight values at p + k, zero from k_end on.
+__device__ inline u32x4 load_k8(const uint16_t *p, int64_t k, int64_t k_end) {
+  if (k + 8 <= k_end) return load16(p + k);
+  u32x4 v = {0, 0, 0, 0};
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+    if (k + i < k_end) v[i >> 1] |= uint32_t(p[k + i]) << (16 * (i & 1));
+  return v;
+}
+
+template <bool F16, int T>
+__global__ void __launch_bounds__(512) few_tokens_kernel(const uint16_t *x, const uint16_t *w,
+                                                         int n, int64_t d_in, int64_t d_out,
+                                                         int kw, int64_t k_part, OutParams out) {
+  constexpr int U = 4;                   // loads of W in flight: 32 k each
+  __shared__ f32x4v s_part[8 * T * 64];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int per_block = int(blockDim.x >> 6) / kw;
+  const int part = wave % kw;
+  const int64_t group = int64_t(blockIdx.x) * per_block + wave / kw;
+  const int64_t f0 = group * 16;
+  const int r = lane & 15, kq = (lane >> 4) * 8;
+  const int64_t feature = f0 + r < d_out ? f0 + r : d_out - 1;   // rows behind the last: unused
+  const uint16_t *pw = w + feature * d_in + kq;
+  const uint16_t *px[T];
+#pragma unroll
+  for (int t = 0; t < T; ++t) {
+    const int tok = t * 16 + r < n ? t * 16 + r : n - 1;
+    px[t] = x + int64_t(tok) * d_in + kq;
+  }
+  f32x4v acc[T];
+#pragma unroll
+  for (int t = 0; t < T; ++t) acc[t] = f32x4v{0, 0, 0, 0};
+
+  const int64_t k0 = part * k_part, k1 = k0 + k_part < d_in ? k0 + k_part : d_in;
+  const int64_t full = k1 > k0 ? (k1 - k0) / (32 * U) : 0;       // whole batches
+  u32x4 cw[U], cx[U][T];
+  auto load = [&](int64_t k, u32x4 (&a)[U], u32x4 (&b)[U][T]) {
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      a[u] = load16(pw + k + 32 * u);
+#pragma unroll
+      for (int t = 0; t < T; ++t) b[u][t] = load16(px[t] + k + 32 * u);
     }
-    default: return 1.0f;
+  };
+  auto use = [&](const u32x4 (&a)[U], const u32x4 (&b)[U][T]) {
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+      for (int t = 0; t < T; ++t) acc[t] = mfma16<F16>(a[u], b[u][t], acc[t]);
+  };
+  if (full > 0) load(k0, cw, cx);
+  for (int64_t i = 1; i < full; ++i) {
+    u32x4 nw[U], nx[U][T];
+    load(k0 + i * (32 * U), nw, nx);
+    use(cw, cx);
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      cw[u] = nw[u];
+#pragma unroll
+      for (int t = 0; t < T; ++t) cx[u][t] = nx[u][t];
+    }
+  }
+  if (full > 0) use(cw, cx);
+  for (int64_t k = k0 + full * (32 * U); k < k1; k += 32) {
+    const u32x4 a = load_k8(pw, k, k1 - kq);
+#pragma unroll
+    for (int t = 0; t < T; ++t) acc[t] = mfma16<F16>(a, load_k8(px[t], k, k1 - kq), acc[t]);
+  }
+
+  auto store = [&](int t, f32x4v v) {
+    // lane: token t*16 + (lane & 15), features f0 + 4 (lane >> 4) .. + 3
+    const int64_t m = f0 + (lane >> 4) * 4, c = t * 16 + r;
+    const int count = m >= d_out ? 0 : (d_out - m >= 4 ? 4 : int(d_out - m));
+    if (c >= n || count == 0) return;
+    float z[4] = {v[0], v[1], v[2], v[3]}, b[4];
+    load_bias<F16, 4>(out, m, count, b);
+    finish<F16, 4>(out, z, b, m, c, count, 0);
+  };
+  if (kw == 1) {
+#pragma unroll
+    for (int t = 0; t < T; ++t) store(t, acc[t]);
+    return;
+  }
+#pragma unroll
+  for (int t = 0; t < T; ++t) s_part[(wave * T + t) * 64 + lane] = acc[t];
+  __syncthreads();
+  for (int t = part; t < T; t += kw) {
+    const int first = wave - part;
+    f32x4v v = s_part[(first * T + t) * 64 + lane];
+    for (int q = 1; q < kw; ++q) v += s_part[((first + q) * T + t) * 64 + lane];
+    store(t, v);
   }
 }
 
-// What becomes of C[m][c], stored at row c, element m of the result.
-struct OutParams {
-  void *out;              // [cols][ld]
+// ---------------------------------------------------------- prepared copies --
+
+// Operands as the tiled cores take them, from any alignment: one launch fills
+// all copies a call needs.  A block turns a 64 x 64 tile of a [rows][cols]
+// matrix into the padded row-major copy (columns behind the last are zero up
+// to ld) and / or the padded transposed one, multiplying by the activation's
+// slope and summing columns on the way where asked.
+struct CopyJob {
+  const void *src;          // [rows][cols], 16-bit, or e4m3 codes with scales
+  const uint8_t *scales;
+  const void *z;            // multiply by act'(z), null: do not
+  const uint8_t *z_scales;
+  int64_t rows, cols;
+  uint16_t *dst;            // [rows][ld], null: none
   int64_t ld;
-  int64_t rows, cols;     // valid m and c
-  const void *bias;       // [rows], 16-bit or fp32, or null
-  const uint16_t *residual;  // [cols][ld] or null
-  uint16_t *preact;       // [cols][ld] or null
-  int32_t out_f32, bias_f32, act, add;   // add: out += C
+  uint16_t *dst_t;          // [cols][ld_t], null: none
+  int64_t ld_t;
+  float *sums;              // [tile rows][cols] sums over 64 rows, null: none
+  int64_t tiles_c, tiles;
+  int32_t act;
+};
+constexpr int kMaxCopies = 3;
+struct CopyJobs {
+  CopyJob job[kMaxCopies];
 };
 
-template <class TR>
-struct OutEpi {
-  OutParams p;
-  static constexpr bool F16 = TR::F16;
-
-  __device__ __forceinline__ void one(float z, int64_t m, int64_t c) const {
-    const int64_t at = c * p.ld + m;
-    if (p.bias)
-      z += p.bias_f32 ? static_cast<const float *>(p.bias)[m]
-                      : widen<F16>(static_cast<const uint16_t *>(p.bias)[m]);
-    if (p.preact) p.preact[at] = narrow<F16>(z);
-    float y = act_value(z, p.act);
-    if (p.residual) y += widen<F16>(p.residual[at]);
-    if (p.out_f32) {
-      float *o = static_cast<float *>(p.out) + at;
-      *o = p.add ? *o + y : y;
-    } else {
-      uint16_t *o = static_cast<uint16_t *>(p.out) + at;
-      *o = narrow<F16>(p.add ? widen<F16>(*o) + y : y);
-    }
+// Eight saved values from column c of a row on, `count` of them.
+template <bool F16>
+__device__ inline void saved8(const void *v, const uint8_t *scales, int64_t row, int64_t cols,
+                              int64_t c, int count, float (&f)[8]) {
+  if (!scales) {
+    read_half<F16, 8>(static_cast<const uint16_t *>(v) + row * cols + c, count, f);
+    return;
   }
-  __device__ __forceinline__ void operator()(typename TR::AccBlock (&acc)[TR::FM][TR::FN],
-                                             int64_t m0, int64_t n0, int wm, int wn, int lane,
-                                             int) const {
-#pragma unroll 1
-    for (int fn = 0; fn < TR::FN; ++fn) {
-      const int64_t c = n0 + wn * TR::WTN + fn * TR::MF + TR::col_of(lane);
-      if (c >= p.cols) continue;
-#pragma unroll 1
-      for (int fm = 0; fm < TR::FM; ++fm) {
+  const uint8_t *p = static_cast<const uint8_t *>(v) + row * cols + c;
+  uint32_t q[2] = {0, 0};
+  if (count == 8) {
+    __builtin_memcpy(q, p, 8);
+  } else {
 #pragma unroll
-        for (int r = 0; r < TR::R; ++r) {
-          const int64_t m = m0 + wm * TR::WTM + fm * TR::MF + TR::row_of(r, lane);
-          float z = 0.0f;
+    for (int i = 0; i < 8; ++i)
+      if (i < count) q[i >> 2] |= uint32_t(p[i]) << (8 * (i & 3));
+  }
+  // (eight columns from a multiple of 8 on share a block of 32)
+  codes_to_f32(q[0], q[1], int(scales[row * ((cols + 31) / 32) + c / 32]) - 127, f);
 #pragma unroll
-          for (int a = 0; a < TR::FM; ++a)
+  for (int i = 0; i < 8; ++i) f[i] = widen<F16>(saturate16<F16>(f[i]));
+}
+
+template <bool F16>
+__global__ void __launch_bounds__(256) copies_kernel(CopyJobs jobs) {
+  __shared__ uint32_t s_t[64 * 33];
+  __shared__ float s_sum[4][64];
+  int64_t b = blockIdx.x;
+  int which = 0;
+  while (which + 1 < kMaxCopies && b >= jobs.job[which].tiles) b -= jobs.job[which++].tiles;
+  const CopyJob &j = jobs.job[which];
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int64_t tr = b / j.tiles_c, r0 = tr * 64, c0 = (b % j.tiles_c) * 64;
+  const int cc = tid & 7, pair = tid >> 3;           // 8 columns, rows 2 pair and 2 pair + 1
+  const int64_t c = c0 + cc * 8;
+  const int count = c >= j.cols ? 0 : (j.cols - c >= 8 ? 8 : int(j.cols - c));
+  float sum[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+  u32x4 v[2] = {u32x4{0, 0, 0, 0}, u32x4{0, 0, 0, 0}};
 #pragma unroll
-            for (int b = 0; b < TR::FN; ++b)
-              if (a == fm && b == fn) z = acc[a][b][r];
-          if (m < p.rows) one(z, m, c);
-        }
+  for (int h = 0; h < 2; ++h) {
+    const int64_t row = r0 + 2 * pair + h;
+    if (row < j.rows && count > 0) {
+      float f[8];
+      saved8<F16>(j.src, j.scales, row, j.cols, c, count, f);
+      if (j.z) {
+        float z[8];
+        saved8<F16>(j.z, j.z_scales, row, j.cols, c, count, z);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) f[i] *= act_slope(z[i], j.act);
       }
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        if (i >= count) f[i] = 0.0f;
+        sum[i] += f[i];
+      }
+      v[h] = narrow8<F16>(f);
+    }
+    if (j.dst && row < j.rows && c < j.ld)
+      *reinterpret_cast<u32x4 *>(j.dst + row * j.ld + c) = v[h];
+  }
+  if (j.dst_t) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const uint32_t lo = (v[0][i >> 1] >> (16 * (i & 1))) & 0xffffu;
+      const uint32_t hi = (v[1][i >> 1] >> (16 * (i & 1))) & 0xffffu;
+      s_t[(cc * 8 + i) * 33 + pair] = lo | (hi << 16);
     }
   }
-};
-
-// ---------------------------------------------------- the backward's inputs --
-
-// Z as 16-bit values or as an 8-bit checkpoint.
-struct Saved {
-  const void *v;           // 16-bit values or codes, [n][d]; null: none
-  const uint8_t *scales;   // [n][ceil(d/32)] for codes, else null
-};
-template <bool F16>
-__device__ inline float saved_value(const Saved &s, int64_t row, int64_t col, int64_t d) {
-  if (!s.scales) return widen<F16>(static_cast<const uint16_t *>(s.v)[row * d + col]);
-  const uint32_t code = static_cast<const uint8_t *>(s.v)[row * d + col];
-  const int e = int(s.scales[row * ((d + 31) / 32) + col / 32]) - 127;
-  const float f = __builtin_ldexpf(__builtin_amdgcn_cvt_f32_fp8(int(code), 0), e);
-  return widen<F16>(saturate16<F16>(f));
-}
-
-// Rows of `rows_per` tokens: G = dY act'(Z) stored when g is given, and the
-// fp32 column sums of the unrounded G over these rows when sums is given
-// ([gridDim.y][d]).  Thread = column.
-template <bool F16>
-__global__ void __launch_bounds__(256) slope_kernel(const uint16_t *dy, Saved z, int64_t n,
-                                                    int64_t d, int act, int64_t rows_per,
-                                                    uint16_t *g, float *sums) {
-  const int64_t col = int64_t(blockIdx.x) * 256 + threadIdx.x;
-  if (col >= d) return;
-  const int64_t r0 = int64_t(blockIdx.y) * rows_per;
-  const int64_t r1 = r0 + rows_per < n ? r0 + rows_per : n;
-  float sum = 0.0f;
-  for (int64_t r = r0; r < r1; ++r) {
-    float v = widen<F16>(dy[r * d + col]);
-    if (z.v) v *= act_slope(saved_value<F16>(z, r, col, d), act);
-    sum += v;
-    if (g) g[r * d + col] = narrow<F16>(v);
+  if (j.sums) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+#pragma unroll
+      for (int o = 8; o < 64; o <<= 1) sum[i] += __shfl_xor(sum[i], o);
+      if (lane < 8) s_sum[wave][cc * 8 + i] = sum[i];
+    }
   }
-  if (sums) sums[int64_t(blockIdx.y) * d + col] = sum;
+  if (!j.dst_t && !j.sums) return;      // block-uniform
+  __syncthreads();
+  if (j.sums && tid < 64 && c0 + tid < j.cols)
+    j.sums[tr * j.cols + c0 + tid] =
+        ((s_sum[0][tid] + s_sum[1][tid]) + s_sum[2][tid]) + s_sum[3][tid];
+  if (j.dst_t) {
+    const int col = tid >> 2, q = tid & 3;
+    const int64_t t0 = r0 + q * 16;
+    if (c0 + col < j.cols && t0 < j.ld_t) {
+      uint32_t w[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) w[i] = s_t[col * 33 + q * 8 + i];
+      u32x4 *d = reinterpret_cast<u32x4 *>(j.dst_t + (c0 + col) * j.ld_t + t0);
+      d[0] = u32x4{w[0], w[1], w[2], w[3]};
+      d[1] = u32x4{w[4], w[5], w[6], w[7]};
+    }
+  }
 }
 
-// Adds `parts` rows of sums in order.
+// Adds the bias gradient's 64-row sums in order.
 template <bool F16>
-__global__ void __launch_bounds__(256) bias_grad_kernel(const float *sums, int64_t parts, int64_t d,
-                                                        void *out, int out_f32, int add) {
-  const int64_t col = int64_t(blockIdx.x) * 256 + threadIdx.x;
+__global__ void __launch_bounds__(64) bias_grad_kernel(const float *sums, int64_t parts, int64_t d,
+                                                       void *out, int out_f32, int add) {
+  const int64_t col = int64_t(blockIdx.x) * 64 + threadIdx.x;
   if (col >= d) return;
   float s = 0.0f;
+#pragma unroll 8
   for (int64_t i = 0; i < parts; ++i) s += sums[i * d + col];
   if (out_f32) {
     float *o = static_cast<float *>(out) + col;
@@ -150,54 +275,264 @@ __global__ void __launch_bounds__(256) bias_grad_kernel(const float *sums, int64
   }
 }
 
+// Adds a product's K-splits ([split][cols][ld] fp32) in order and finishes.
+template <bool F16>
+__global__ void __launch_bounds__(256) fold_kernel(const float *part, int64_t ld, int64_t stride,
+                                                   int splits, OutParams out) {
+  const int64_t per_row = ld / 8, total = per_row * out.cols;
+  for (int64_t u = int64_t(blockIdx.x) * 256 + threadIdx.x; u < total;
+       u += int64_t(gridDim.x) * 256) {
+    const int64_t c = u / per_row, m = (u - c * per_row) * 8;
+    const int count = out.rows - m >= 8 ? 8 : int(out.rows - m);
+    float z[8] = {0, 0, 0, 0, 0, 0, 0, 0}, b[8];
+    const float *p = part + c * ld + m;
+    for (int s = 0; s < splits; ++s, p += stride) {
+      const u32x4 x = *reinterpret_cast<const u32x4 *>(p);
+      const u32x4 y = *reinterpret_cast<const u32x4 *>(p + 4);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        z[i] += __uint_as_float(x[i]);
+        z[4 + i] += __uint_as_float(y[i]);
+      }
+    }
+    load_bias<F16, 8>(out, m, count, b);
+    finish<F16, 8>(out, z, b, m, c, count, 0);
+  }
+}
+
 // ------------------------------------------------------------------- host --
 
-template <class TR, bool AK, bool BKM>
-static void run_product(const void *A, int64_t lda, const void *B, int64_t ldb, int64_t M,
-                        int64_t N, int64_t K, const OutParams &out, hipStream_t st) {
-  const bool vec = aligned_to(A, 16) && aligned_to(B, 16) && lda % 8 == 0 && ldb % 8 == 0;
-  GemmParams g = {};
-  g.A = A; g.lda = lda; g.B = B; g.ldb = ldb;
-  g.M = M; g.N = N; g.K = K;
-  g.M_read = round_to(M, 8); g.N_read = round_to(N, 8);
-  g.k_per_split = round_to(K, TR::BK);
-  g.tiles_n = ceil_div(N, TR::BN);
-  const int64_t tiles = ceil_div(M, TR::BM) * g.tiles_n;
-  const OutEpi<TR> epi{out};
-  if (vec) gemm_kernel<TR, AK, BKM, true><<<dim3(uint32_t(tiles)), TR::NT, 0, st>>>(g, epi);
-  else gemm_kernel<TR, AK, BKM, false><<<dim3(uint32_t(tiles)), TR::NT, 0, st>>>(g, epi);
-}
-
-// Rows of dY that one block of slope_kernel sums.
-static int64_t slope_rows(int64_t n) {
-  const int64_t r = ceil_div(n, 256);
-  return r < 16 ? 16 : r;
-}
-
-struct LinearPlan {
-  size_t off_g = 0, off_x = 0, off_sums = 0, total = 0;
-  int64_t sum_parts = 0;
+// How one product C[m][c], m < M, c < N, depth K runs.
+struct ProductPlan {
+  int tile = 0;             // 256: the 256 x 256 core, 128, 64: tile_kernel, 0: the generic one
+  int64_t splits = 1, k_per_split = 0;
+  size_t part_bytes = 0;    // fp32 partial results of the splits
 };
 
-static int32_t plan_linear(int64_t n, int64_t d_in, int64_t d_out, int32_t dtype) {
-  if (const int32_t st = lce_dims_check(n, d_in, d_out); st != LCE_OK) return st;
-  return half_type(dtype) ? LCE_OK : LCE_DTYPE_MISMATCH;
+struct Operand {
+  const void *p;
+  int64_t ld;
+};
+
+static int64_t tile_count(int64_t M, int64_t N, int t) { return ceil_div(M, t) * ceil_div(N, t); }
+
+// Modelled microseconds of a 64-deep step of one tile on a compute unit that
+// it shares with no other (256) or with what fits beside it (128, 64).
+static ProductPlan plan_product(int64_t M, int64_t N, int64_t K) {
+  ProductPlan best;
+  double best_us = 1e30;
+  const int64_t steps = ceil_div(K, 64);
+  for (const int t : {256, 128, 64}) {
+    const double step_us = t == 256 ? 1.43 : t == 128 ? 0.55 : 0.25;
+    const double fixed_us = t == 256 ? 8.0 : 3.0;
+    const int64_t at_once = t == 256 ? 256 : t == 128 ? 256 : 512;   // tiles running at a time
+    const int64_t tiles = tile_count(M, N, t);
+    for (int64_t sp = 1; sp <= 16 && sp <= steps; sp *= 2) {
+      const int64_t per = ceil_div(steps, sp);
+      if ((sp - 1) * per >= steps) continue;
+      const double rounds = double(ceil_div(tiles * sp, at_once));
+      double us = rounds * (fixed_us + per * step_us);
+      if (sp > 1) us += 4.0 + double(M) * double(N) * 4.0 * 2.0 * double(sp) / 4.5e6;
+      if (us < best_us) {
+        best_us = us;
+        best.tile = t;
+        best.splits = sp;
+        best.k_per_split = per * 64;
+      }
+    }
+  }
+  best.part_bytes = best.splits > 1 ? size_t(best.splits * N * round_to(M, 8)) * 4 : 0;
+  return best;
 }
-static int32_t plan_linear_backward(int64_t n, int64_t d_in, int64_t d_out, int32_t dtype,
-                                    LinearPlan *p) {
-  if (const int32_t st = plan_linear(n, d_in, d_out, dtype); st != LCE_OK) return st;
-  p->sum_parts = ceil_div(n, slope_rows(n));
+
+// The register-staged core of the losses: any alignment, 64-bit offsets.
+template <class TR>
+struct DirectEpi {
+  OutParams p;
+  __device__ __forceinline__ void operator()(typename TR::AccBlock (&acc)[TR::FM][TR::FN],
+                                             int64_t m0, int64_t n0, int wm, int wn, int lane,
+                                             int) const {
+    // (rolled loops with the block picked by selects: 16 copies of the
+    // epilogue would not be unrolled and the accumulators would go to memory)
+#pragma unroll 1
+    for (int f = 0; f < TR::FM * TR::FN; ++f) {
+      const int fm = f / TR::FN, fn = f % TR::FN;
+      const int64_t c = n0 + wn * TR::WTN + fn * TR::MF + TR::col_of(lane);
+      f32x16 blk = acc[0][0];
+#pragma unroll
+      for (int a = 0; a < TR::FM; ++a)
+#pragma unroll
+        for (int b = 0; b < TR::FN; ++b)
+          if (a == fm && b == fn) blk = acc[a][b];
+      if (c >= p.cols) continue;
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const int64_t m = m0 + wm * TR::WTM + fm * TR::MF + TR::row_of(4 * q, lane);
+        const int count = m >= p.rows ? 0 : (p.rows - m >= 4 ? 4 : int(p.rows - m));
+        float z[4], b[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) z[i] = blk[4 * q + i];
+        load_bias<TR::F16, 4>(p, m, count, b);
+        if (count > 0) finish<TR::F16, 4>(p, z, b, m, c, count, 0);
+      }
+    }
+  }
+};
+template <bool F16, bool AK, bool BKM>
+static void run_generic(Operand A, Operand B, int64_t M, int64_t N, int64_t K,
+                        const OutParams &out, hipStream_t st) {
+  typedef TraitsH16<F16> TR;
+  GemmParams g = {};
+  g.A = A.p; g.lda = A.ld; g.B = B.p; g.ldb = B.ld;
+  g.M = M; g.N = N; g.K = K;
+  g.k_per_split = round_to(K, TR::BK);
+  g.tiles_n = ceil_div(N, TR::BN);
+  const uint32_t tiles = uint32_t(tile_count(M, N, 256));
+  gemm_kernel<TR, AK, BKM, false><<<tiles, TR::NT, 0, st>>>(g, DirectEpi<TR>{out});
+}
+
+// Runs a planned product of padded, aligned operands.  AK, BKM: the operand
+// is K-major (the small tiles take K-major ones only).
+template <bool F16, bool AK, bool BKM>
+static void run_product(const ProductPlan &pl, Operand A, Operand B, int64_t M, int64_t N,
+                        int64_t K, const OutParams &out, char *part, hipStream_t st) {
+  OutParams o = out;
+  if (pl.splits > 1) {
+    o = {};
+    o.out = part;
+    o.ld = round_to(M, 8);
+    o.rows = out.rows;
+    o.cols = out.cols;
+    o.out_f32 = 1;
+    o.split_stride = N * o.ld;
+  }
+  if (pl.tile == 0) {
+    run_generic<F16, AK, BKM>(A, B, M, N, K, out, st);
+  } else if (pl.tile == 256) {
+    typedef TraitsH16W8<F16> TR;
+    typedef PipeCfg<64, 2> CFG;
+    Gemm2Params g = {};
+    g.A = A.p; g.lda = A.ld; g.B = B.p; g.ldb = B.ld;
+    g.M = M; g.N = N; g.K = K;
+    g.M_read = A.ld; g.N_read = B.ld;
+    g.k_per_split = pl.k_per_split;
+    g.tiles_n = ceil_div(N, 256);
+    const int64_t wgs = tile_count(M, N, 256) * pl.splits;
+    gemm2_kernel<CFG, TR, AK, BKM, OutEpi<TR>><<<uint32_t(wgs), TR::NT, 0, st>>>(g, OutEpi<TR>{o});
+  } else if constexpr (AK && BKM) {
+    TileParams g = {};
+    g.A = A.p; g.lda = A.ld; g.B = B.p; g.ldb = B.ld;
+    g.M = M; g.N = N; g.K = K;
+    g.k_per_split = pl.k_per_split;
+    g.tiles_n = int32_t(ceil_div(N, pl.tile));
+    g.tiles = int32_t(tile_count(M, N, pl.tile));
+    const uint32_t wgs = uint32_t(g.tiles * pl.splits);
+    if (pl.tile == 128) {
+      typedef Tile<128, 128, 2, 2, 2, F16> T;
+      tile_kernel<T><<<wgs, T::NT, 0, st>>>(g, OutEpi<T>{o});
+    } else {
+      typedef Tile<64, 64, 2, 2, 4, F16> T;
+      tile_kernel<T><<<wgs, T::NT, 0, st>>>(g, OutEpi<T>{o});
+    }
+  }
+  if (pl.splits > 1) {
+    const int64_t blocks = ceil_div(o.ld / 8 * out.cols, 256);
+    fold_kernel<F16><<<uint32_t(blocks < 4096 ? blocks : 4096), 256, 0, st>>>(
+        reinterpret_cast<const float *>(part), o.ld, o.split_stride, int(pl.splits), out);
+  }
+}
+
+// The tiled cores address 256 rows of an operand with 32-bit byte offsets.
+static bool offsets_fit(int64_t ld) { return 256 * ld * 2 < (int64_t(1) << 31); }
+
+constexpr int64_t kFewTokens = 64;
+
+struct LinearPlan {
+  bool few = false;
+  ProductPlan product;
+  int64_t ld_in = 0;                      // padded d_in of the copies, 0: no copies
+  size_t off_x = 0, off_w = 0, off_part = 0, total = 0;
+};
+
+struct BackwardPlan {
+  ProductPlan px, pw;                     // d_x and d_weight
+  int64_t ld_in = 0, ld_out = 0, ld_n = 0;
+  int64_t sum_parts = 0;
+  size_t off_g = 0, off_gt = 0, off_x = 0, off_xt = 0, off_w = 0, off_wt = 0;
+  size_t off_part = 0, off_sums = 0, total = 0;
+};
+
+struct Layout {
   size_t at = 0;
-  auto take = [&](int64_t bytes) {
+  size_t take(size_t bytes) {
     const size_t here = at;
-    at += size_t(round_to(bytes, 256));
+    at += size_t(round_to(int64_t(bytes), 256));
     return here;
-  };
-  p->off_g = take(n * d_out * 2);
-  p->off_x = take(n * d_in * 2);
-  p->off_sums = take(p->sum_parts * d_out * 4);
-  p->total = at + 256;
+  }
+};
+
+static int32_t plan_linear(int64_t n, int64_t d_in, int64_t d_out, int32_t dtype, LinearPlan *p) {
+  if (const int32_t st = lce_dims_check(n, d_in, d_out); st != LCE_OK) return st;
+  if (!half_type(dtype)) return LCE_DTYPE_MISMATCH;
+  p->few = n <= kFewTokens;
+  if (p->few) return LCE_OK;
+  Layout l;
+  p->product = plan_product(d_out, n, d_in);
+  if (d_in % (p->product.tile == 256 ? 64 : 8) != 0) {
+    p->ld_in = round_to(d_in, 64);
+    p->off_x = l.take(size_t(n * p->ld_in * 2));
+    p->off_w = l.take(size_t(d_out * p->ld_in * 2));
+  }
+  p->off_part = l.take(p->product.part_bytes);
+  p->total = l.at ? l.at + 256 : 0;
   return LCE_OK;
+}
+
+static int32_t plan_linear_backward(int64_t n, int64_t d_in, int64_t d_out, int32_t dtype,
+                                    BackwardPlan *p) {
+  if (const int32_t st = lce_dims_check(n, d_in, d_out); st != LCE_OK) return st;
+  if (!half_type(dtype)) return LCE_DTYPE_MISMATCH;
+  Layout l;
+  p->px = plan_product(d_in, n, d_out);
+  p->pw = plan_product(d_in, d_out, n);
+  p->ld_in = round_to(d_in, 64);
+  p->ld_out = round_to(d_out, 64);
+  p->ld_n = round_to(n, 64);
+  if (!offsets_fit(p->ld_out)) p->px = p->pw = ProductPlan{};
+  else if (!offsets_fit(p->ld_n) && p->pw.tile != 256) p->pw = ProductPlan{};
+  p->sum_parts = ceil_div(n, 64);
+  p->off_g = l.take(size_t(n * p->ld_out * 2));
+  if (p->px.tile == 256 || p->px.tile == 0) p->off_w = l.take(size_t(d_out * p->ld_in * 2));
+  else p->off_wt = l.take(size_t(d_in * p->ld_out * 2));
+  if (p->pw.tile == 256 || p->pw.tile == 0) {
+    p->off_x = l.take(size_t(n * p->ld_in * 2));
+  } else {
+    p->off_gt = l.take(size_t(d_out * p->ld_n * 2));
+    p->off_xt = l.take(size_t(d_in * p->ld_n * 2));
+  }
+  p->off_part = l.take(p->px.part_bytes > p->pw.part_bytes ? p->px.part_bytes : p->pw.part_bytes);
+  p->off_sums = l.take(size_t(p->sum_parts * d_out * 4));
+  p->total = l.at + 256;
+  return LCE_OK;
+}
+
+template <bool F16>
+static void run_copies(CopyJobs &jobs, int count, hipStream_t st) {
+  int64_t blocks = 0;
+  for (int i = 0; i < kMaxCopies; ++i) {
+    CopyJob &j = jobs.job[i];
+    if (i >= count) {
+      j.tiles = 0;
+      j.tiles_c = 1;
+      continue;
+    }
+    // tiles up to the padded columns of dst and the padded rows of dst_t: the
+    // padding ends inside the last tile (multiples of 64)
+    j.tiles_c = ceil_div(j.cols, 64);
+    j.tiles = ceil_div(j.rows, 64) * j.tiles_c;
+    blocks += j.tiles;
+  }
+  if (blocks) copies_kernel<F16><<<uint32_t(blocks), 256, 0, st>>>(jobs);
 }
 
 static bool known_act(int32_t a) { return a >= LCE_ACT_NONE && a <= LCE_ACT_SILU; }
@@ -217,48 +552,138 @@ static int32_t check_saved(const lce_tensor *v, const lce_tensor *scales, int32_
 }
 
 template <bool F16>
-static void linear_run(const lce_tensor *x, const lce_tensor *w, const OutParams &out, int64_t n,
-                       int64_t d_in, int64_t d_out, hipStream_t st) {
-  run_product<TraitsH16<F16>, true, true>(w->data, d_in, x->data, d_in, d_out, n, d_in, out, st);
+static void linear_run(const LinearPlan &p, const lce_tensor *x, const lce_tensor *w,
+                       const OutParams &out, int64_t n, int64_t d_in, int64_t d_out, char *ws,
+                       hipStream_t st) {
+  if (p.few) {
+    const int64_t groups = ceil_div(d_out, 16);
+    // waves that share 16 rows: until about 2048 waves run, 128 k each at least
+    int kw = 1;
+    while (kw < 8 && groups * kw < 2048 && d_in / (2 * kw) >= 128) kw *= 2;
+    const int waves = kw > 4 ? kw : 4, per_block = waves / kw;
+    const int64_t k_part = round_to(ceil_div(d_in, kw), 32);
+    auto run = [&](auto kernel) {
+      kernel<<<uint32_t(ceil_div(groups, per_block)), waves * 64, 0, st>>>(
+          static_cast<const uint16_t *>(x->data), static_cast<const uint16_t *>(w->data), int(n),
+          d_in, d_out, kw, k_part, out);
+    };
+    if (n <= 16) run(few_tokens_kernel<F16, 1>);
+    else if (n <= 32) run(few_tokens_kernel<F16, 2>);
+    else run(few_tokens_kernel<F16, 4>);
+    return;
+  }
+  Operand X = {x->data, d_in}, W = {w->data, d_in};
+  if (p.ld_in) {
+    CopyJobs jobs = {};
+    const Operand src[2] = {X, W};
+    const int64_t rows[2] = {n, d_out};
+    const size_t off[2] = {p.off_x, p.off_w};
+    Operand *to[2] = {&X, &W};
+    for (int i = 0; i < 2; ++i) {
+      CopyJob &j = jobs.job[i];
+      j.src = src[i].p; j.rows = rows[i]; j.cols = d_in;
+      j.dst = reinterpret_cast<uint16_t *>(ws + off[i]); j.ld = p.ld_in;
+      *to[i] = {j.dst, p.ld_in};
+    }
+    run_copies<F16>(jobs, 2, st);
+  } else if (!aligned_to(X.p, 16) || !aligned_to(W.p, 16)) {
+    run_generic<F16, true, true>(W, X, d_out, n, d_in, out, st);
+    return;
+  }
+  run_product<F16, true, true>(p.product, W, X, d_out, n, p.ld_in ? p.ld_in : d_in, out,
+                               ws + p.off_part, st);
 }
 
 template <bool F16>
-static void linear_backward_run(const LinearPlan &p, const lce_tensor *dy, const lce_tensor *x,
-                                const lce_tensor *x_scales, const lce_tensor *w, const Saved &z,
-                                int64_t n, int64_t d_in, int64_t d_out, int32_t act,
-                                lce_tensor *d_x, lce_tensor *d_w, lce_tensor *d_b, int32_t add,
-                                char *ws, void *stream) {
-  typedef TraitsH16<F16> TR;
-  const hipStream_t st = hipStream_t(stream);
-  const uint16_t *G = static_cast<const uint16_t *>(dy->data);
+static void linear_backward_run(const BackwardPlan &p, const lce_tensor *dy, const lce_tensor *x,
+                                const lce_tensor *x_scales, const lce_tensor *w,
+                                const lce_tensor *z, const lce_tensor *z_scales, int64_t n,
+                                int64_t d_in, int64_t d_out, int32_t act, lce_tensor *d_x,
+                                lce_tensor *d_w, lce_tensor *d_b, int32_t add, char *ws,
+                                hipStream_t st) {
+  auto at = [&](size_t off) { return reinterpret_cast<uint16_t *>(ws + off); };
+  auto scales_of = [](const lce_tensor *t) {
+    return given(t) ? static_cast<const uint8_t *>(t->data) : nullptr;
+  };
+  const bool want_x = given(d_x), want_w = given(d_w), want_b = given(d_b);
   const bool slope = act != kNone;
-  if (slope || given(d_b)) {
-    uint16_t *g = slope ? reinterpret_cast<uint16_t *>(ws + p.off_g) : nullptr;
-    float *sums = given(d_b) ? reinterpret_cast<float *>(ws + p.off_sums) : nullptr;
-    slope_kernel<F16><<<dim3(uint32_t(ceil_div(d_out, 256)), uint32_t(p.sum_parts)), 256, 0, st>>>(
-        G, slope ? z : Saved{nullptr, nullptr}, n, d_out, act, slope_rows(n), g, sums);
-    if (given(d_b))
-      bias_grad_kernel<F16><<<uint32_t(ceil_div(d_out, 256)), 256, 0, st>>>(
-          sums, p.sum_parts, d_out, d_b->data, d_b->dtype == LCE_F32, add);
-    if (slope) G = g;
-  }
-  OutParams o = {};
-  if (given(d_x)) {
-    o.out = d_x->data; o.ld = d_in; o.rows = d_in; o.cols = n;
-    run_product<TR, false, true>(w->data, d_in, G, d_out, d_in, n, d_out, o, st);
-  }
-  if (given(d_w)) {
-    const void *X = x->data;
-    if (given(x_scales)) {
-      lce_tensor xt = {ws + p.off_x, n * d_in, F16 ? LCE_F16 : LCE_BF16};
-      lce_unpack8(x, x_scales, n, d_in, &xt, stream);
-      X = xt.data;
+  // which copies the products need; what is aligned and of the right kind
+  // already is used where it lies
+  CopyJobs jobs = {};
+  int count = 0;
+  Operand G = {dy->data, d_out}, GT = {nullptr, 0}, X = {nullptr, 0}, W = {nullptr, 0};
+  // (the small tiles take transposed copies, the others operands as they lie)
+  const bool small_x = want_x && (p.px.tile == 128 || p.px.tile == 64);
+  const bool small_w = want_w && (p.pw.tile == 128 || p.pw.tile == 64);
+  const bool big_x = want_x && !small_x, big_w = want_w && !small_w;
+  const bool copy_g = slope || !aligned_to(dy->data, 16) ||
+                      (big_x && d_out % 64 != 0) || d_out % 8 != 0;
+  {
+    CopyJob j = {};
+    j.src = dy->data; j.rows = n; j.cols = d_out;
+    if (slope) {
+      j.z = z->data; j.z_scales = scales_of(z_scales);
+      j.act = act;
     }
+    if (copy_g && (want_x || big_w)) {
+      j.dst = at(p.off_g); j.ld = p.ld_out;
+      G = {j.dst, j.ld};
+    }
+    if (small_w) {
+      j.dst_t = at(p.off_gt); j.ld_t = p.ld_n;
+      GT = {j.dst_t, j.ld_t};
+    }
+    if (want_b) j.sums = reinterpret_cast<float *>(ws + p.off_sums);
+    if (j.dst || j.dst_t || j.sums) jobs.job[count++] = j;
+  }
+  if (want_w) {
+    CopyJob j = {};
+    j.src = x->data; j.scales = scales_of(x_scales);
+    j.rows = n; j.cols = d_in;
+    if (small_w) {
+      j.dst_t = at(p.off_xt); j.ld_t = p.ld_n;
+      X = {j.dst_t, j.ld_t};
+    } else if (j.scales || !aligned_to(x->data, 16) || d_in % 8 != 0) {
+      j.dst = at(p.off_x); j.ld = p.ld_in;
+      X = {j.dst, j.ld};
+    } else {
+      X = {x->data, d_in};
+    }
+    if (j.dst || j.dst_t) jobs.job[count++] = j;
+  }
+  if (want_x) {
+    CopyJob j = {};
+    j.src = w->data; j.rows = d_out; j.cols = d_in;
+    if (small_x) {
+      j.dst_t = at(p.off_wt); j.ld_t = p.ld_out;
+      W = {j.dst_t, j.ld_t};
+    } else if (!aligned_to(w->data, 16) || d_in % 8 != 0) {
+      j.dst = at(p.off_w); j.ld = p.ld_in;
+      W = {j.dst, j.ld};
+    } else {
+      W = {w->data, d_in};
+    }
+    if (j.dst || j.dst_t) jobs.job[count++] = j;
+  }
+  run_copies<F16>(jobs, count, st);
+
+  if (want_b)
+    bias_grad_kernel<F16><<<uint32_t(ceil_div(d_out, 64)), 64, 0, st>>>(
+        reinterpret_cast<const float *>(ws + p.off_sums), p.sum_parts, d_out, d_b->data,
+        d_b->dtype == LCE_F32, add);
+  OutParams o = {};
+  if (want_x) {
+    o.out = d_x->data; o.ld = d_in; o.rows = d_in; o.cols = n;
+    if (big_x) run_product<F16, false, true>(p.px, W, G, d_in, n, d_out, o, ws + p.off_part, st);
+    else run_product<F16, true, true>(p.px, W, G, d_in, n, round_to(d_out, 8), o, ws + p.off_part, st);
+  }
+  if (want_w) {
     o = {};
     o.out = d_w->data; o.ld = d_in; o.rows = d_in; o.cols = d_out;
     o.out_f32 = d_w->dtype == LCE_F32;
     o.add = add;
-    run_product<TR, false, false>(X, d_in, G, d_out, d_in, d_out, n, o, st);
+    if (big_w) run_product<F16, false, false>(p.pw, X, G, d_in, d_out, n, o, ws + p.off_part, st);
+    else run_product<F16, true, true>(p.pw, X, GT, d_in, d_out, p.ld_n, o, ws + p.off_part, st);
   }
 }
 
@@ -269,13 +694,14 @@ using namespace lce;
 extern "C" {
 
 int64_t lce_linear_workspace_bytes(int64_t n_tok, int64_t d_in, int64_t d_out, int32_t dtype) {
-  const int32_t st = plan_linear(n_tok, d_in, d_out, dtype);
-  return st == LCE_OK ? 256 : -int64_t(st);
+  LinearPlan p;
+  const int32_t st = plan_linear(n_tok, d_in, d_out, dtype, &p);
+  return st == LCE_OK ? int64_t(p.total) : -int64_t(st);
 }
 
 int64_t lce_linear_backward_workspace_bytes(int64_t n_tok, int64_t d_in, int64_t d_out,
                                             int32_t dtype) {
-  LinearPlan p;
+  BackwardPlan p;
   const int32_t st = plan_linear_backward(n_tok, d_in, d_out, dtype, &p);
   return st == LCE_OK ? int64_t(p.total) : -int64_t(st);
 }
@@ -285,18 +711,20 @@ int32_t lce_linear(const lce_tensor *x, const lce_tensor *weight, const lce_tens
                    int32_t activation, lce_tensor *preact, lce_tensor *out, lce_tensor *workspace,
                    void *stream) {
   if (const int32_t st = lce_dims_check(n_tok, d_in, d_out); st != LCE_OK) return st;
-  if (!x || !weight || !out || !workspace) return LCE_LENGTH_MISMATCH;
+  if (!x || !weight || !out) return LCE_LENGTH_MISMATCH;
   const int32_t dt = x->dtype;
   if (!half_type(dt) || weight->dtype != dt || (out->dtype != dt && out->dtype != LCE_F32) ||
       (given(bias) && bias->dtype != dt && bias->dtype != LCE_F32) ||
       (given(residual) && residual->dtype != dt) || (given(preact) && preact->dtype != dt) ||
-      workspace->dtype != LCE_U8)
+      (given(workspace) && workspace->dtype != LCE_U8))
     return LCE_DTYPE_MISMATCH;
+  LinearPlan p;
+  (void)plan_linear(n_tok, d_in, d_out, dt, &p);
   const int64_t cells = n_tok * d_out;
   if (!holds(x, n_tok * d_in) || !holds(weight, d_out * d_in) || !holds(out, cells) ||
       (given(bias) && bias->numel < d_out) || (given(residual) && residual->numel < cells) ||
       (given(preact) && preact->numel < cells) ||
-      !holds(workspace, lce_linear_workspace_bytes(n_tok, d_in, d_out, dt)))
+      (p.total && !holds(workspace, int64_t(p.total))))
     return LCE_LENGTH_MISMATCH;
   if (!known_act(activation)) return LCE_UNKNOWN_OBJECTIVE;
 
@@ -310,8 +738,9 @@ int32_t lce_linear(const lce_tensor *x, const lce_tensor *weight, const lce_tens
   o.bias_f32 = given(bias) && bias->dtype == LCE_F32;
   o.act = activation;
   const hipStream_t st = hipStream_t(stream);
-  if (dt == LCE_F16) linear_run<true>(x, weight, o, n_tok, d_in, d_out, st);
-  else linear_run<false>(x, weight, o, n_tok, d_in, d_out, st);
+  char *ws = p.total ? aligned_base(workspace) : nullptr;
+  if (dt == LCE_F16) linear_run<true>(p, x, weight, o, n_tok, d_in, d_out, ws, st);
+  else linear_run<false>(p, x, weight, o, n_tok, d_in, d_out, ws, st);
   return enqueued_status();
 }
 
@@ -340,7 +769,7 @@ int32_t lce_linear_backward(const lce_tensor *d_out_grad, const lce_tensor *x,
       if (const int32_t st = check_saved(preact, preact_scales, dt, n_tok, d_out, lengths); st != LCE_OK)
         return st;
   }
-  LinearPlan p;
+  BackwardPlan p;
   (void)plan_linear_backward(n_tok, d_in, d_out, dt, &p);
   if (!holds(d_out_grad, n_tok * d_out) || (given(d_x) && (!holds(weight, d_out * d_in) || !holds(d_x, n_tok * d_in))) ||
       (given(d_weight) && !holds(d_weight, d_out * d_in)) ||
@@ -349,16 +778,16 @@ int32_t lce_linear_backward(const lce_tensor *d_out_grad, const lce_tensor *x,
   if (!known_act(activation)) return LCE_UNKNOWN_OBJECTIVE;
 
   (void)hipGetLastError();
-  const Saved z = {slope ? preact->data : nullptr,
-                   slope && given(preact_scales)
-                       ? static_cast<const uint8_t *>(preact_scales->data) : nullptr};
   char *ws = aligned_base(workspace);
+  const hipStream_t st = hipStream_t(stream);
   if (dt == LCE_F16)
-    linear_backward_run<true>(p, d_out_grad, x, x_scales, weight, z, n_tok, d_in, d_out, activation,
-                              d_x, d_weight, d_bias, accumulate != 0, ws, stream);
+    linear_backward_run<true>(p, d_out_grad, x, x_scales, weight, preact, preact_scales, n_tok,
+                              d_in, d_out, activation, d_x, d_weight, d_bias, accumulate != 0, ws,
+                              st);
   else
-    linear_backward_run<false>(p, d_out_grad, x, x_scales, weight, z, n_tok, d_in, d_out,
-                               activation, d_x, d_weight, d_bias, accumulate != 0, ws, stream);
+    linear_backward_run<false>(p, d_out_grad, x, x_scales, weight, preact, preact_scales, n_tok,
+                               d_in, d_out, activation, d_x, d_weight, d_bias, accumulate != 0,
+                               ws, st);
   return enqueued_status();
 }
 

@@ -1,0 +1,330 @@
+// ops_gemm.hpp -- 16-bit product C[m][c] = sum_k A[m][k] B[c][k] on the matrix
+// cores for tiles smaller than the 256 x 256 core of lce_gemm2.hpp, and the
+// epilogue that both share.
+//
+// Both operands are K-major with leading dimensions that are multiples of 8
+// and 16-byte aligned bases.  Stages of 64 k go global -> LDS by DMA (no
+// registers in between) into a ring of STAGES buffers, STAGES - 1 ahead; a
+// k-step is one wait for its own stage, one barrier, the issue of the stage
+// that takes the buffer just freed, and 4 MFMA substeps.  Chunks behind the
+// last k and rows behind the last row are fetched from behind the buffer's
+// end, which reads as zero.
+#pragma once
+
+#include "../csrc/lce_gemm2.hpp"
+#include "ops_common.h"
+
+namespace lce {
+
+enum Act { kNone = LCE_ACT_NONE, kRelu = LCE_ACT_RELU, kGelu = LCE_ACT_GELU, kSilu = LCE_ACT_SILU };
+
+__device__ inline float act_value(float z, int act) {
+  switch (act) {
+    case kRelu: return z > 0.0f || z != z ? z : 0.0f;
+    case kGelu: return 0.5f * z * (1.0f + erff(z * 0.70710678118654752f));
+    case kSilu: return z / (1.0f + __expf(-z));
+    default: return z;
+  }
+}
+__device__ inline float act_slope(float z, int act) {
+  switch (act) {
+    case kRelu: return z > 0.0f ? 1.0f : 0.0f;
+    case kGelu:
+      return 0.5f * (1.0f + erff(z * 0.70710678118654752f)) +
+             z * 0.39894228040143268f * __expf(-0.5f * z * z);
+    case kSilu: {
+      const float s = 1.0f / (1.0f + __expf(-z));
+      return s * (1.0f + z * (1.0f - s));
+    }
+    default: return 1.0f;
+  }
+}
+
+// ------------------------------------------------------------- epilogue --
+
+// What becomes of C[m][c], element m of row c of the result.
+struct OutParams {
+  void *out;                 // [cols][ld]
+  int64_t ld;
+  int64_t rows, cols;        // valid m and c
+  const void *bias;          // [rows], 16-bit or fp32, or null
+  const uint16_t *residual;  // [cols][ld] or null
+  uint16_t *preact;          // [cols][ld] or null
+  int64_t split_stride;      // elements between the splits' results (fp32)
+  int32_t out_f32, bias_f32, act, add;   // add: out += C
+};
+
+// The bias of elements m .. m + W - 1, of which `count` exist (0 behind).
+template <bool F16, int W>
+__device__ inline void load_bias(const OutParams &p, int64_t m, int count, float (&b)[W]) {
+#pragma unroll
+  for (int i = 0; i < W; ++i) b[i] = 0.0f;
+  if (!p.bias) return;
+#pragma unroll
+  for (int i = 0; i < W; ++i)
+    if (i < count)
+      b[i] = p.bias_f32 ? static_cast<const float *>(p.bias)[m + i]
+                        : widen<F16>(static_cast<const uint16_t *>(p.bias)[m + i]);
+}
+
+// W (4 or 8) consecutive 16-bit or fp32 values at any alignment; the first
+// `count` of them exist.
+template <bool F16, int W>
+__device__ inline void read_half(const uint16_t *p, int count, float (&f)[W]) {
+  if (count == W) {
+    uint32_t v[W / 2];
+    __builtin_memcpy(v, __builtin_assume_aligned(p, 2), W * 2);
+#pragma unroll
+    for (int i = 0; i < W / 2; ++i) {
+      f[2 * i] = widen<F16>(uint16_t(v[i]));
+      f[2 * i + 1] = widen<F16>(uint16_t(v[i] >> 16));
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < W; ++i) f[i] = i < count ? widen<F16>(p[i]) : 0.0f;
+  }
+}
+template <bool F16, int W>
+__device__ inline void write_half(uint16_t *p, int count, const float (&f)[W]) {
+  if (count == W) {
+    uint32_t v[W / 2];
+#pragma unroll
+    for (int i = 0; i < W / 2; ++i)
+      v[i] = uint32_t(narrow<F16>(f[2 * i])) | (uint32_t(narrow<F16>(f[2 * i + 1])) << 16);
+    __builtin_memcpy(__builtin_assume_aligned(p, 2), v, W * 2);
+  } else {
+#pragma unroll
+    for (int i = 0; i < W; ++i)
+      if (i < count) p[i] = narrow<F16>(f[i]);
+  }
+}
+
+// Elements m .. m + W - 1 of row c of split `split`: z the sums, b the bias.
+template <bool F16, int W>
+__device__ __forceinline__ void finish(const OutParams &p, float (&z)[W], const float (&b)[W],
+                                       int64_t m, int64_t c, int count, int split) {
+  const int64_t at = c * p.ld + m;
+#pragma unroll
+  for (int i = 0; i < W; ++i) z[i] += b[i];
+  if (p.preact) write_half<F16, W>(p.preact + at, count, z);
+  if (p.act != kNone) {
+#pragma unroll
+    for (int i = 0; i < W; ++i) z[i] = act_value(z[i], p.act);
+  }
+  if (p.residual) {
+    float r[W];
+    read_half<F16, W>(p.residual + at, count, r);
+#pragma unroll
+    for (int i = 0; i < W; ++i) z[i] += r[i];
+  }
+  if (p.out_f32) {
+    float *o = static_cast<float *>(p.out) + split * p.split_stride + at;
+    if (count == W) {
+      if (p.add) {
+        float r[W];
+        __builtin_memcpy(r, __builtin_assume_aligned(o, 4), W * 4);
+#pragma unroll
+        for (int i = 0; i < W; ++i) z[i] += r[i];
+      }
+      __builtin_memcpy(__builtin_assume_aligned(o, 4), z, W * 4);
+    } else {
+#pragma unroll
+      for (int i = 0; i < W; ++i)
+        if (i < count) o[i] = p.add ? o[i] + z[i] : z[i];
+    }
+  } else {
+    uint16_t *o = static_cast<uint16_t *>(p.out) + at;
+    if (p.add) {
+      float r[W];
+      read_half<F16, W>(o, count, r);
+#pragma unroll
+      for (int i = 0; i < W; ++i) z[i] += r[i];
+    }
+    write_half<F16, W>(o, count, z);
+  }
+}
+
+// Epilogue of both cores: a wave passes its accumulators through its own part
+// of LDS, 32 rows of the result at a time, so that global accesses are 16
+// bytes a lane along the rows.  The 16-byte chunks of an LDS row are XORed
+// with the row's number, which spreads the column-wise writes over the banks.
+template <class TR>
+struct OutEpi {
+  OutParams p;
+  static constexpr bool kStaged = true;
+  static constexpr int CH = TR::WTM / 4;                  // 16-byte chunks per row
+  static constexpr int MASK = CH < 16 ? CH - 1 : 15;
+  static constexpr int BYTES = 32 * TR::WTM * 4;          // LDS per wave
+
+  __device__ __forceinline__ void staged(typename TR::AccBlock (&acc)[TR::FM][TR::FN], int64_t m0,
+                                         int64_t n0, int wm, int wn, int lane, int split,
+                                         char *lds, const char *) const {
+    const int64_t mw = m0 + wm * TR::WTM, cw = n0 + wn * TR::WTN;
+    if (mw >= p.rows || cw >= p.cols) return;             // wave-uniform
+    char *region = lds + (wm * TR::WAVES_N + wn) * BYTES;
+    constexpr int LPR = TR::WTM / 8;                      // lanes per row
+    const int j = lane % LPR, r0 = lane / LPR;
+    const int64_t m = mw + j * 8;
+    const int count = m >= p.rows ? 0 : (p.rows - m >= 8 ? 8 : int(p.rows - m));
+    float b[8];
+    load_bias<TR::F16, 8>(p, m, count, b);
+#pragma unroll
+    for (int fn = 0; fn < TR::FN; ++fn) {
+      const int row = lane & 31;
+#pragma unroll
+      for (int fm = 0; fm < TR::FM; ++fm)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const int ch = fm * 8 + 2 * q + (lane >> 5);
+          f32x4 v;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) v[i] = acc[fm][fn][4 * q + i];
+          *reinterpret_cast<f32x4 *>(region + row * (TR::WTM * 4) + ((ch ^ (row & MASK)) << 4)) = v;
+        }
+      asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+#pragma unroll 1
+      for (int i = 0; i < 32 * LPR / 64; ++i) {
+        const int rr = r0 + i * (64 / LPR);
+        const char *q = region + rr * (TR::WTM * 4);
+        const f32x4 a = *reinterpret_cast<const f32x4 *>(q + (((2 * j) ^ (rr & MASK)) << 4));
+        const f32x4 c = *reinterpret_cast<const f32x4 *>(q + (((2 * j + 1) ^ (rr & MASK)) << 4));
+        float z[8] = {a[0], a[1], a[2], a[3], c[0], c[1], c[2], c[3]};
+        const int64_t col = cw + fn * 32 + rr;
+        if (col < p.cols && count > 0) finish<TR::F16, 8>(p, z, b, m, col, count, split);
+      }
+      asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");   // read before it is overwritten
+    }
+  }
+  typedef float f32x4 __attribute__((ext_vector_type(4)));
+};
+
+// ------------------------------------------------------------------ core --
+
+template <int BM_, int BN_, int WM_, int WN_, int ST_, bool F16_>
+struct Tile {
+  static constexpr bool F16 = F16_;
+  typedef f32x16 AccBlock;
+  static constexpr int BM = BM_, BN = BN_, BK = 64, STAGES = ST_;
+  static constexpr int WAVES_M = WM_, WAVES_N = WN_, NW = WM_ * WN_, NT = NW * 64;
+  static constexpr int WTM = BM / WM_, WTN = BN / WN_, FM = WTM / 32, FN = WTN / 32;
+  static constexpr int STAGE_BYTES = (BM + BN) * 128;
+  static constexpr int RING = STAGES * STAGE_BYTES;
+  static constexpr int EPI = NW * 32 * WTM * 4;
+  static constexpr int LDS = RING > EPI ? RING : EPI;
+  static_assert(BM % (8 * NW) == 0 && BN % (8 * NW) == 0, "whole loads per wave");
+};
+
+struct TileParams {
+  const void *A, *B;
+  int64_t lda, ldb;          // elements
+  int64_t M, N, K;           // K a multiple of 8
+  int64_t k_per_split;       // multiple of 64
+  int32_t tiles_n, tiles;    // tiles of one split
+};
+
+// ROWS rows of one operand.
+template <class T, int ROWS>
+struct TileOperand {
+  static constexpr int INSTR = ROWS / 8 / T::NW;    // 1 KB loads per wave and stage
+  __amdgpu_buffer_rsrc_t rs;
+  uint32_t voff[INSTR];      // byte offset of this lane's chunk at k = 0
+  int kc[INSTR];             // its k within a stage
+
+  __device__ inline void init(const void *p, int64_t ld, int64_t row0, int64_t rows, int wave,
+                              int lane) {
+    const uint16_t *base = static_cast<const uint16_t *>(p) + row0 * ld;
+    rs = make_rsrc(base, (rows - row0) * ld * 2);
+#pragma unroll
+    for (int i = 0; i < INSTR; ++i) {
+      const int r = (wave * INSTR + i) * 8 + lane / 8;
+      kc[i] = ((lane & 7) ^ kswz<128>(r)) * 8;
+      voff[i] = uint32_t(r) * uint32_t(ld * 2) + uint32_t(kc[i] * 2);
+    }
+  }
+  template <bool TAIL>
+  __device__ inline void issue(int64_t k0, int64_t k_end, char *dst, int wave) const {
+#pragma unroll
+    for (int i = 0; i < INSTR; ++i) {
+      uint32_t off = voff[i] + uint32_t(k0 * 2);
+      if (TAIL && k0 + kc[i] >= k_end) off = 0x80000000u;     // behind the end: zero
+      dma16<0>(rs, dst + (wave * INSTR + i) * 1024, off);
+    }
+  }
+  static __device__ inline u32x4 frag(const char *src, int base, int kk, int lane) {
+    const int r = base + (lane & 31), c = kk * 2 + (lane >> 5);
+    return *reinterpret_cast<const u32x4 *>(src + r * 128 + ((c ^ kswz<128>(r)) << 4));
+  }
+};
+
+// One tile of one split; `bid` of `tiles * splits` workgroups.
+template <class T, class Epi>
+__device__ __forceinline__ void tile_block(const TileParams &g, const Epi &epi, int64_t bid,
+                                           char *smem) {
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int wm = wave / T::WAVES_N, wn = wave % T::WAVES_N;
+  const int split = int(bid / g.tiles), t = int(bid % g.tiles);
+  const int64_t m0 = int64_t(t / g.tiles_n) * T::BM, n0 = int64_t(t % g.tiles_n) * T::BN;
+  const int64_t kb = split * g.k_per_split;
+  const int64_t ke = kb + g.k_per_split < g.K ? kb + g.k_per_split : g.K;
+  const int n_k = ke > kb ? int((ke - kb + 63) / 64) : 0;
+
+  TileOperand<T, T::BM> oa;
+  TileOperand<T, T::BN> ob;
+  oa.init(g.A, g.lda, m0, g.M, wave, lane);
+  ob.init(g.B, g.ldb, n0, g.N, wave, lane);
+  constexpr int LPS = TileOperand<T, T::BM>::INSTR + TileOperand<T, T::BN>::INSTR;
+  auto issue = [&](int s) {
+    char *st = smem + (s % T::STAGES) * T::STAGE_BYTES;
+    const int64_t k0 = kb + int64_t(s) * 64;
+    if (k0 + 64 <= ke) {
+      oa.template issue<false>(k0, ke, st, wave);
+      ob.template issue<false>(k0, ke, st + T::BM * 128, wave);
+    } else {
+      oa.template issue<true>(k0, ke, st, wave);
+      ob.template issue<true>(k0, ke, st + T::BM * 128, wave);
+    }
+  };
+
+  f32x16 acc[T::FM][T::FN];
+#pragma unroll
+  for (int a = 0; a < T::FM; ++a)
+#pragma unroll
+    for (int b = 0; b < T::FN; ++b)
+#pragma unroll
+      for (int r = 0; r < 16; ++r) acc[a][b][r] = 0.0f;
+
+#pragma unroll
+  for (int s = 0; s < T::STAGES - 1; ++s)
+    if (s < n_k) issue(s);
+  for (int it = 0; it < n_k; ++it) {
+    // stage `it` has landed everywhere, and every wave is done with stage it - 1
+    wait_vm_barrier_stages<LPS, T::STAGES - 2>(n_k - 1 - it);
+    if (it + T::STAGES - 1 < n_k) issue(it + T::STAGES - 1);
+    const char *sa = smem + (it % T::STAGES) * T::STAGE_BYTES, *sb = sa + T::BM * 128;
+#pragma unroll
+    for (int kk = 0; kk < 4; ++kk) {
+      u32x4 fa[T::FM], fb[T::FN];
+#pragma unroll
+      for (int a = 0; a < T::FM; ++a)
+        fa[a] = TileOperand<T, T::BM>::frag(sa, wm * T::WTM + a * 32, kk, lane);
+#pragma unroll
+      for (int b = 0; b < T::FN; ++b)
+        fb[b] = TileOperand<T, T::BN>::frag(sb, wn * T::WTN + b * 32, kk, lane);
+#pragma unroll
+      for (int a = 0; a < T::FM; ++a)
+#pragma unroll
+        for (int b = 0; b < T::FN; ++b) acc[a][b] = mfma32<T>(fa[a], fb[b], acc[a][b]);
+    }
+  }
+  __syncthreads();     // the ring becomes the epilogue's staging space
+  epi.staged(acc, m0, n0, wm, wn, lane, split, smem, nullptr);
+}
+
+template <class T, class Epi>
+__global__ void __launch_bounds__(T::NT) tile_kernel(TileParams g, Epi epi) {
+  __shared__ __attribute__((aligned(1024))) char smem[T::LDS];
+  tile_block<T>(g, epi, xcd_remap(blockIdx.x, gridDim.x), smem);
+}
+
+}  // namespace lce

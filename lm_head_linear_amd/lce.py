@@ -763,7 +763,8 @@ def linear(x, weight, bias=None, residual=None, activation="none", want_preact=F
             nbytes = lce_linear_workspace_bytes(n, d_in, d_out, x.dtype)
             if nbytes < 0:
                 raise LceError(int(-nbytes), "lce_linear_workspace_bytes")
-            workspace = torch.empty(nbytes, dtype=torch.uint8, device=dev)
+            if nbytes > 0:
+                workspace = torch.empty(nbytes, dtype=torch.uint8, device=dev)
         out = torch.empty(n, d_out, dtype=out_dtype or x.dtype, device=dev)
         preact = torch.empty(n, d_out, dtype=x.dtype, device=dev) if want_preact else None
         _check(lce_linear(x, weight, bias, residual, n, d_in, d_out,
