@@ -8,17 +8,19 @@
 // logits; only those meet across beams, in fp64.
 //
 // Selection, bound by the read of the logits: every block of 256 threads holds
-// one piece of a row in registers (32 values a thread, so the loads of a
+// one piece of a row in registers (8 VECS values a thread, so the loads of a
 // piece are all in flight together and nothing is read twice), takes the
 // piece's maximum and sum of exponentials, and finds its n_out largest values
-// by a threshold: with the 256 threads in 64 groups, the n_out-th largest
-// group maximum T has at least n_out values at or above it, all held by a few
-// threads, so the values >= T (typically a few more than n_out) go to a list
-// in LDS and the list is ranked by counting.  A piece in which more values
-// than the list holds reach T (long ties) finds the exact cut by bisection on
-// (value, token) keys, which are all different.
+// by a threshold: with the 256 threads in 64 groups of four, the n_out-th
+// largest group maximum T has at least n_out values at or above it, all held
+// by a few threads, so the values >= T (typically a few more than n_out) go to
+// a list in LDS and the list is ranked by counting.  T is found by bisecting
+// on the bits of the ordered value with one ballot a step, a group maximum a
+// lane.  A piece in which more values than the list holds reach T (long ties)
+// finds the exact cut by bisection on (value, token) keys, which are all
+// different.
 // A second kernel, one block per sequence, folds the pieces' sums in fp64 and
-// ranks the candidates of all beams by the same threshold.
+// ranks the candidates of all beams by the same kind of threshold.
 #include <math.h>
 
 #include "ops_common.h"
@@ -26,12 +28,11 @@
 namespace lce {
 
 constexpr int kBeamThreads = 256;
-constexpr int kBeamVecs = 4;                                     // 8-value vectors per thread
-constexpr int kBeamPiece = kBeamThreads * kBeamVecs * 8;         // values of a row per block
 constexpr int kBeamGroups = 64;                                  // threshold groups per block
 constexpr int kBeamList = 1024;                                  // candidates a block can list
 constexpr int64_t kMaxBeams = 32, kMaxBeamOut = 64;
 static_assert(kMaxBeamOut <= kBeamGroups, "the threshold needs n_out groups");
+static_assert(LCE_MAX_VOCAB <= (1 << 24) && kMaxBeams <= 128, "a place is beam << 24 | token");
 
 // fp32 in an unsigned order (-0 counts as +0); 0 is below every number.
 __device__ inline uint32_t order32(float x) {
@@ -56,40 +57,98 @@ struct PieceStats {
   int32_t pad;
 };
 
-template <class T> struct Logit;   // eight values at p as fp32
+// Eight logits as they lie in memory, and as fp32.
+template <class T> struct Logit;
 template <bool F16> struct Half8 {};
 template <bool F16> struct Logit<Half8<F16>> {
   typedef uint16_t E;
-  __device__ static inline void load8(const E *p, float (&f)[8]) { widen8<F16>(load16(p), f); }
+  struct Vec { u32x4 a; };
+  __device__ static inline Vec load8(const E *p) { return Vec{load16(p)}; }
   __device__ static inline float load1(const E *p) { return widen<F16>(*p); }
+  __device__ static inline void values(const Vec &v, float (&f)[8]) { widen8<F16>(v.a, f); }
+  __device__ static inline Vec nothing() {
+    const uint32_t none = F16 ? 0xfc00fc00u : 0xff80ff80u;
+    return Vec{u32x4{none, none, none, none}};
+  }
+  // -inf in place i
+  __device__ static inline void blank(Vec &v, int i) {
+    const uint32_t none = F16 ? 0xfc00u : 0xff80u;
+    v.a[i >> 1] = i & 1 ? (v.a[i >> 1] & 0xffffu) | (none << 16) : (v.a[i >> 1] & 0xffff0000u) | none;
+  }
+  __device__ static inline void put(Vec &v, int i, E x) {
+    v.a[i >> 1] = i & 1 ? (v.a[i >> 1] & 0xffffu) | (uint32_t(x) << 16)
+                        : (v.a[i >> 1] & 0xffff0000u) | x;
+  }
+  // makes the values opaque: they are widened again where they are used again
+  // (kept as fp32 they would take twice the registers)
+  __device__ static inline void hold(Vec &v) { asm volatile("" : "+v"(v.a)); }
 };
 template <> struct Logit<float> {
   typedef float E;
-  __device__ static inline void load8(const E *p, float (&f)[8]) {
-    const u32x4 a = load16(p), b = load16(p + 4);
+  struct Vec { u32x4 a, b; };
+  __device__ static inline Vec load8(const E *p) { return Vec{load16(p), load16(p + 4)}; }
+  __device__ static inline float load1(const E *p) { return *p; }
+  __device__ static inline void values(const Vec &v, float (&f)[8]) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      f[i] = __uint_as_float(a[i]);
-      f[4 + i] = __uint_as_float(b[i]);
+      f[i] = __uint_as_float(v.a[i]);
+      f[4 + i] = __uint_as_float(v.b[i]);
     }
   }
-  __device__ static inline float load1(const E *p) { return *p; }
+  __device__ static inline Vec nothing() {
+    const uint32_t none = 0xff800000u;
+    return Vec{u32x4{none, none, none, none}, u32x4{none, none, none, none}};
+  }
+  __device__ static inline void put(Vec &v, int i, E x) {
+    (i < 4 ? v.a : v.b)[i & 3] = __float_as_uint(x);
+  }
+  __device__ static inline void blank(Vec &v, int i) { put(v, i, -INFINITY); }
+  __device__ static inline void hold(Vec &v) { asm volatile("" : "+v"(v.a), "+v"(v.b)); }
 };
 
+// Lane swaps within a row of 16 lanes (DPP: no LDS), then one lane of each of
+// the wave's four rows: the result is uniform.
+#define LCE_ROW16(x, op)                                                                \
+  x = op(x, __builtin_bit_cast(decltype(x), __builtin_amdgcn_mov_dpp(__builtin_bit_cast(int, x), 0xB1, 0xF, 0xF, true)));  /* 1 0 3 2 */       \
+  x = op(x, __builtin_bit_cast(decltype(x), __builtin_amdgcn_mov_dpp(__builtin_bit_cast(int, x), 0x4E, 0xF, 0xF, true)));  /* 2 3 0 1 */       \
+  x = op(x, __builtin_bit_cast(decltype(x), __builtin_amdgcn_mov_dpp(__builtin_bit_cast(int, x), 0x141, 0xF, 0xF, true))); /* half mirror */   \
+  x = op(x, __builtin_bit_cast(decltype(x), __builtin_amdgcn_mov_dpp(__builtin_bit_cast(int, x), 0x140, 0xF, 0xF, true)))  /* mirror */
+__device__ inline float row_lane(float x, int lane) {
+  return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(x), lane));
+}
+__device__ inline float add_f(float a, float b) { return a + b; }
+__device__ inline int add_i(int a, int b) { return a + b; }
+__device__ inline float wave_max(float x) {
+  LCE_ROW16(x, fmaxf);
+  return fmaxf(fmaxf(row_lane(x, 0), row_lane(x, 16)), fmaxf(row_lane(x, 32), row_lane(x, 48)));
+}
+// 16 fp32 terms at a time, the rest in fp64.
+__device__ inline double wave_sum_rows(float x) {
+  LCE_ROW16(x, add_f);
+  return (double(row_lane(x, 0)) + row_lane(x, 16)) + (double(row_lane(x, 32)) + row_lane(x, 48));
+}
+__device__ inline int wave_sum(int x) {
+  LCE_ROW16(x, add_i);
+  return __builtin_amdgcn_readlane(x, 0) + __builtin_amdgcn_readlane(x, 16) +
+         __builtin_amdgcn_readlane(x, 32) + __builtin_amdgcn_readlane(x, 48);
+}
 __device__ inline double wave_sum(double x) {
 #pragma unroll
   for (int o = 32; o > 0; o >>= 1) x += __shfl_xor(x, o);
   return x;
 }
-__device__ inline int wave_sum(int x) {
+
+// The largest value with BITS leading bits that at least `want` of the wave's
+// keys reach (0 when fewer are above 0).
+template <int BITS>
+__device__ inline uint32_t wave_cut(uint32_t key, int want) {
+  uint32_t cut = 0;
 #pragma unroll
-  for (int o = 32; o > 0; o >>= 1) x += __shfl_xor(x, o);
-  return x;
-}
-__device__ inline float wave_max(float x) {
-#pragma unroll
-  for (int o = 32; o > 0; o >>= 1) x = fmaxf(x, __shfl_xor(x, o));
-  return x;
+  for (int bit = 31; bit > 31 - BITS; --bit) {
+    const uint32_t next = cut | (1u << bit);
+    if (__popcll(__builtin_amdgcn_ballot_w64(key >= next)) >= want) cut = next;
+  }
+  return cut;
 }
 
 // Candidates of one piece, best first: (order32(value) << 32) | ~token.
@@ -97,19 +156,23 @@ __device__ inline uint64_t piece_key(float x, uint32_t token) {
   return (uint64_t(order32(x)) << 32) | uint32_t(~token);
 }
 
-// Block (piece, row): cand[row][piece][n_out] and stats[row][piece].
-template <class T>
-__global__ void __launch_bounds__(kBeamThreads) beam_piece_kernel(
+// Block (row, piece): cand[row][piece][n_out] and stats[row][piece].
+// (16-bit logits: at most 80 registers, so that six waves a SIMD keep the
+// memory busy while others compute)
+template <class T, int VECS, bool MASK>
+__global__ void __launch_bounds__(kBeamThreads, sizeof(typename Logit<T>::E) == 2 ? 6 : 3)
+    beam_piece_kernel(
     const typename Logit<T>::E *logits, const uint8_t *allowed, const uint8_t *finished,
     int64_t vocab, int pieces, int n_out, uint64_t *cand, PieceStats *stats) {
-  const int64_t row = blockIdx.x / pieces;
-  const int piece = int(blockIdx.x % pieces);
+  constexpr int PIECE = kBeamThreads * VECS * 8;
+  const uint32_t row = blockIdx.x / uint32_t(pieces);
+  const int piece = int(blockIdx.x - row * uint32_t(pieces));
   if (finished && finished[row]) return;     // nothing of the row is read
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  const int64_t base = int64_t(piece) * kBeamPiece;
+  const int64_t base = int64_t(piece) * PIECE;
   const int64_t left = vocab - base;         // values of the row from here on
   const typename Logit<T>::E *p = logits + row * vocab + base;
-  const uint8_t *ok = allowed ? allowed + row * vocab + base : nullptr;
+  const uint8_t *ok = MASK ? allowed + row * vocab + base : nullptr;
 
   __shared__ float s_top[4];
   __shared__ double s_sum[4];
@@ -118,33 +181,54 @@ __global__ void __launch_bounds__(kBeamThreads) beam_piece_kernel(
   __shared__ int s_count;
   __shared__ uint64_t s_list[kBeamList];
 
-  float f[kBeamVecs][8];
+  typedef typename Logit<T>::Vec Vec;
+  Vec x[VECS];
+  if (left >= PIECE) {          // block-uniform: all of the piece in flight at once
 #pragma unroll
-  for (int v = 0; v < kBeamVecs; ++v) {
-    const int at = (v * kBeamThreads + tid) * 8;
-    if (at + 8 <= left) {
-      Logit<T>::load8(p + at, f[v]);
-      if (ok) {
-        const AnyVec8 m = *reinterpret_cast<const AnyVec8 *>(ok + at);
+    for (int v = 0; v < VECS; ++v) x[v] = Logit<T>::load8(p + (v * kBeamThreads + tid) * 8);
+    if constexpr (MASK) {
+      AnyVec8 m[VECS];
+#pragma unroll
+      for (int v = 0; v < VECS; ++v)
+        m[v] = *reinterpret_cast<const AnyVec8 *>(ok + (v * kBeamThreads + tid) * 8);
+#pragma unroll
+      for (int v = 0; v < VECS; ++v)
 #pragma unroll
         for (int i = 0; i < 8; ++i)
-          if (((m.v[i >> 2] >> (8 * (i & 3))) & 0xff) == 0) f[v][i] = -INFINITY;
-      }
-    } else {
+          if (((m[v].v[i >> 2] >> (8 * (i & 3))) & 0xff) == 0) Logit<T>::blank(x[v], i);
+    }
+  } else {
 #pragma unroll
-      for (int i = 0; i < 8; ++i)
-        f[v][i] = at + i < left && (!ok || ok[at + i]) ? Logit<T>::load1(p + at + i) : -INFINITY;
+    for (int v = 0; v < VECS; ++v) {
+      const int at = (v * kBeamThreads + tid) * 8;
+      x[v] = Logit<T>::nothing();
+      if (at + 8 <= left) {
+        x[v] = Logit<T>::load8(p + at);
+        if constexpr (MASK) {
+          const AnyVec8 m = *reinterpret_cast<const AnyVec8 *>(ok + at);
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            if (((m.v[i >> 2] >> (8 * (i & 3))) & 0xff) == 0) Logit<T>::blank(x[v], i);
+        }
+      } else if (at < left) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          if (at + i < left && (!MASK || ok[at + i])) Logit<T>::put(x[v], i, p[at + i]);
+      }
     }
   }
   // NaN is passed over by fmaxf and shows in the sum.
   float mine = -INFINITY;
 #pragma unroll
-  for (int v = 0; v < kBeamVecs; ++v)
+  for (int v = 0; v < VECS; ++v) {
+    float f[8];
+    Logit<T>::values(x[v], f);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) mine = fmaxf(mine, f[v][i]);
-  // groups of four neighbouring threads
-  float group = fmaxf(mine, __shfl_xor(mine, 1));
-  group = fmaxf(group, __shfl_xor(group, 2));
+    for (int i = 0; i < 8; i += 2) mine = fmaxf(mine, fmaxf(f[i], f[i + 1]));
+    __builtin_amdgcn_sched_barrier(0);
+  }
+  float group = fmaxf(mine, __int_as_float(__builtin_amdgcn_mov_dpp(__float_as_int(mine), 0xB1, 0xF, 0xF, true)));
+  group = fmaxf(group, __int_as_float(__builtin_amdgcn_mov_dpp(__float_as_int(group), 0x4E, 0xF, 0xF, true)));
   if ((lane & 3) == 0) s_group[tid >> 2] = group;
   float top = wave_max(group);
   if (lane == 0) s_top[wave] = top;
@@ -152,88 +236,103 @@ __global__ void __launch_bounds__(kBeamThreads) beam_piece_kernel(
   __syncthreads();
   top = fmaxf(fmaxf(s_top[0], s_top[1]), fmaxf(s_top[2], s_top[3]));
   const float m = top == -INFINITY ? 0.0f : top;
-  float sum = 0.0f;
+  // exp(x - m) = 2^(x L - m L): m L as the rounded hi that the fma subtracts
+  // and an exact rest that scales the sum
+  const float L2E = 1.4426950408889634f, hi = m * L2E, lo = fmaf(m, L2E, -hi);
+  float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-  for (int v = 0; v < kBeamVecs; ++v)
+  for (int v = 0; v < VECS; ++v) {
+    float f[8];
+    Logit<T>::hold(x[v]);
+    Logit<T>::values(x[v], f);
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
-      sum += __builtin_amdgcn_exp2f((f[v][i] - m) * 1.4426950408889634f);
-  const double wsum = wave_sum(double(sum));
-  if (lane == 0) s_sum[wave] = wsum;
-  // the n_out-th largest group maximum: the group whose rank is n_out - 1,
-  // equal ones by place
-  if (wave == 0) {
-    const float g = s_group[lane];
-    int rank = 0;
-    for (int j = 0; j < kBeamGroups; ++j) {
-      const float o = s_group[j];
-      rank += (o > g || (o == g && j < lane)) ? 1 : 0;
-    }
-    if (rank == n_out - 1) s_cut = g;
+    for (int i = 0; i < 8; ++i) sum[i & 3] += __builtin_amdgcn_exp2f(fmaf(f[i], L2E, -hi));
+    __builtin_amdgcn_sched_barrier(0);      // (widened values of one vector at a time)
   }
+  const double wsum = wave_sum_rows((sum[0] + sum[1]) + (sum[2] + sum[3]));
+  if (lane == 0) s_sum[wave] = wsum;
+  // one wave finds the cut; 16 bits tell all bf16 values apart
+  if (wave == 0) {
+    const uint32_t group_key = order32(s_group[lane]);
+    const uint32_t none = order32(-INFINITY);
+    const uint32_t key = wave_cut<16>(group_key > none ? group_key : 0, n_out);
+    if (lane == 0) s_cut = unorder32(key > none ? key : none + 1);   // -inf is no candidate
+  }
+  __syncthreads();
+  const float cut = s_cut;
+  // which of the thread's values reach the cut; the few that do are read again
+  uint32_t reach[(VECS + 3) / 4];
+#pragma unroll
+  for (int w = 0; w < (VECS + 3) / 4; ++w) reach[w] = 0;
+#pragma unroll
+  for (int v = 0; v < VECS; ++v) {
+    float f[8];
+    Logit<T>::hold(x[v]);
+    Logit<T>::values(x[v], f);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) reach[v / 4] |= f[i] >= cut ? 1u << (8 * (v & 3) + i) : 0u;
+    __builtin_amdgcn_sched_barrier(0);
+  }
+#pragma unroll
+  for (int w = 0; w < (VECS + 3) / 4; ++w)
+    while (reach[w] != 0) {
+      const int bit = __builtin_ctz(reach[w]);
+      reach[w] &= reach[w] - 1;
+      const int idx = ((w * 4 + bit / 8) * kBeamThreads + tid) * 8 + (bit & 7);
+      const int at = atomicAdd(&s_count, 1);
+      if (at < kBeamList) s_list[at] = piece_key(Logit<T>::load1(p + idx), uint32_t(base) + idx);
+    }
   __syncthreads();
   if (tid == 0) {
     PieceStats st;
-    st.sum = ((s_sum[0] + s_sum[1]) + s_sum[2]) + s_sum[3];
+    st.sum = (((s_sum[0] + s_sum[1]) + s_sum[2]) + s_sum[3]) * double(__builtin_amdgcn_exp2f(-lo));
     st.top = top;
     st.pad = 0;
-    stats[row * pieces + piece] = st;
+    stats[int64_t(row) * pieces + piece] = st;
   }
-  // list the values at or above the cut (-inf is no candidate)
-  const float cut = s_cut;
-  if (mine >= cut) {
-#pragma unroll
-    for (int v = 0; v < kBeamVecs; ++v)
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        if (f[v][i] >= cut && f[v][i] > -INFINITY) {
-          const int at = atomicAdd(&s_count, 1);
-          if (at < kBeamList)
-            s_list[at] = piece_key(f[v][i], uint32_t(base) + (v * kBeamThreads + tid) * 8 + i);
-        }
-      }
-  }
-  __syncthreads();
   int count = s_count;
   if (count > kBeamList) {
-    // Bisection: the largest key that n_out keys reach.  The keys of the
-    // listed values are all different and at least n_out of them exist.
+    // Bisection: the largest key that n_out keys reach, a key being the value's
+    // order and the place in the piece, lower places first: all different, and
+    // at least n_out of them exist.  The values are read again in every step.
+    constexpr int PLACE = 16;
+    static_assert(PIECE <= 1 << PLACE, "places in a piece");
     __shared__ int s_n[4];
-    uint64_t lo = 0, hi = ~uint64_t(0);     // reached by >= n_out, by < n_out
-    while (hi - lo > 1) {
-      const uint64_t mid = lo + (hi - lo) / 2;
+    auto key_at = [&](int idx) {
+      if (idx >= left || (MASK && !ok[idx])) return uint64_t(0);
+      const float value = Logit<T>::load1(p + idx);
+      return value >= cut ? (uint64_t(order32(value)) << PLACE) | uint32_t((1 << PLACE) - 1 - idx)
+                          : uint64_t(0);
+    };
+    uint64_t lo_key = uint64_t(order32(cut)) << PLACE;                    // reached by >= n_out
+    uint64_t hi_key = (uint64_t(order32(top)) << PLACE) + (1 << PLACE);   // by none
+    while (hi_key - lo_key > 1) {
+      const uint64_t mid = lo_key + (hi_key - lo_key) / 2;
       int c = 0;
-#pragma unroll
-      for (int v = 0; v < kBeamVecs; ++v)
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-          c += f[v][i] > -INFINITY &&
-               piece_key(f[v][i], uint32_t(base) + (v * kBeamThreads + tid) * 8 + i) >= mid;
+      for (int idx = tid; idx < PIECE; idx += kBeamThreads) c += key_at(idx) >= mid ? 1 : 0;
       c = wave_sum(c);
       if (lane == 0) s_n[wave] = c;
       __syncthreads();
       c = s_n[0] + s_n[1] + s_n[2] + s_n[3];
       __syncthreads();
-      if (c >= n_out) lo = mid;
-      else hi = mid;
+      if (c >= n_out) lo_key = mid;
+      else hi_key = mid;
       if (c == n_out) break;
     }
     if (tid == 0) s_count = 0;
     __syncthreads();
-#pragma unroll
-    for (int v = 0; v < kBeamVecs; ++v)
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const uint64_t key = piece_key(f[v][i], uint32_t(base) + (v * kBeamThreads + tid) * 8 + i);
-        if (f[v][i] > -INFINITY && key >= lo) {
-          const int at = atomicAdd(&s_count, 1);
-          if (at < kBeamList) s_list[at] = key;
-        }
+    for (int idx = tid; idx < PIECE; idx += kBeamThreads) {
+      const uint64_t key = key_at(idx);
+      if (key >= lo_key) {
+        const int at = atomicAdd(&s_count, 1);
+        if (at < kBeamList)
+          s_list[at] = piece_key(unorder32(uint32_t(key >> PLACE)), uint32_t(base) + idx);
       }
+    }
     __syncthreads();
     count = s_count;
   }
-  uint64_t *out = cand + (row * pieces + piece) * n_out;
+  uint64_t *out = cand + (int64_t(row) * pieces + piece) * n_out;
   for (int i = tid; i < count; i += kBeamThreads) {
     const uint64_t key = s_list[i];
     int rank = 0;
@@ -244,146 +343,156 @@ __global__ void __launch_bounds__(kBeamThreads) beam_piece_kernel(
 }
 
 // A candidate of a sequence: larger total first, then the lower place
-// beam * vocab + token.
+// (beam << 24 | token).
 struct BeamKey {
   uint64_t total;    // order64(total), 0: none
-  uint64_t place;
+  uint32_t place;
 };
-__device__ inline bool before(uint64_t ta, uint64_t pa, uint64_t tb, uint64_t pb) {
-  return ta > tb || (ta == tb && pa < pb);
+__device__ inline bool before(const BeamKey &a, const BeamKey &b) {
+  return a.total > b.total || (a.total == b.total && a.place < b.place);
+}
+
+// (m, s) += (m2, s2) where s counts exp(x - m): the larger maximum carries on.
+__device__ inline void fold_sum(double &m, double &s, double m2, double s2) {
+  if (m2 > m) {
+    const double t = m;
+    m = m2; m2 = t;
+    const double u = s;
+    s = s2; s2 = u;
+  }
+  // (a maximum of -inf comes with a sum of 0, or of NaN, which stays)
+  s += s2 == 0.0 ? 0.0 : s2 * exp(m2 - m);
 }
 
 // One block per sequence.
 __global__ void __launch_bounds__(kBeamThreads) beam_merge_kernel(
     const uint64_t *cand, const PieceStats *stats, const float *scores, const uint8_t *finished,
-    int beams, int64_t vocab, int pieces, int n_out, int64_t eos, float *out_scores,
-    int64_t *out_parents, int64_t *out_tokens, uint8_t *out_finished) {
+    int beams, int pieces, int n_out, int64_t eos, float *out_scores, int64_t *out_parents,
+    int64_t *out_tokens, uint8_t *out_finished) {
   const int64_t seq = blockIdx.x;
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  __shared__ double s_shift[kMaxBeams];     // score - lse, or the score of a finished beam
   __shared__ double s_lse[kMaxBeams];
-  __shared__ int8_t s_state[kMaxBeams];     // 0: offers nothing, 1: open, 2: finished
-  __shared__ BeamKey s_best[kBeamThreads];
-  __shared__ BeamKey s_list[kBeamList];
-  __shared__ BeamKey s_cut;
+  __shared__ int s_state[kMaxBeams];        // 0: offers nothing, 1: open, 2: finished
+  __shared__ uint64_t s_total[kBeamList];
+  __shared__ uint32_t s_place[kBeamList];
+  __shared__ uint32_t s_group[kBeamGroups];
   __shared__ int s_count;
 
-  // normalisers: one wave a beam, its lanes over the pieces
-  for (int k = wave; k < beams; k += kBeamThreads / 64) {
+  // normalisers: 32 lanes a beam, each folding the pieces it meets
+  const int per_beam = pieces * n_out;
+  for (int k = tid >> 5; k < beams; k += kBeamThreads / 32) {
     const int64_t row = seq * beams + k;
     const float score = scores[row];
-    int state;
-    double lse = 0.0;
-    if (finished && finished[row]) {
-      state = isfinite(score) ? 2 : 0;
-    } else {
-      float top = -INFINITY;
-      for (int c = lane; c < pieces; c += 64) top = fmaxf(top, stats[row * pieces + c].top);
-      top = wave_max(top);
-      const double m = top == -INFINITY ? 0.0 : double(top);
-      double sum = 0.0;
-      for (int c = lane; c < pieces; c += 64) {
+    const bool done = finished && finished[row];
+    double m = -INFINITY, sum = 0.0;
+    if (!done) {
+      for (int c = tid & 31; c < pieces; c += 32) {
         const PieceStats st = stats[row * pieces + c];
-        sum += st.top == -INFINITY && st.sum == 0.0 ? 0.0 : st.sum * exp(double(st.top) - m);
+        fold_sum(m, sum, double(st.top), st.sum);
       }
-      lse = m + log(wave_sum(sum));
-      state = isfinite(score) && isfinite(lse) ? 1 : 0;   // NaN, +inf or nothing allowed: none
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) fold_sum(m, sum, __shfl_xor(m, o), __shfl_xor(sum, o));
     }
-    if (lane == 0) {
-      s_lse[k] = lse;
-      s_state[k] = int8_t(state);
+    if ((tid & 31) == 0) {
+      const double lse = m + log(sum);
+      s_lse[k] = done ? 0.0 : lse;
+      s_shift[k] = score;
+      // NaN, +inf or nothing allowed: the beam offers nothing
+      s_state[k] = !isfinite(score) ? 0 : done ? 2 : isfinite(lse) ? 1 : 0;
     }
   }
   if (tid == 0) s_count = 0;
   __syncthreads();
 
-  const int64_t per_beam = int64_t(pieces) * n_out, total_cand = beams * per_beam;
-  auto candidate = [&](int64_t i) {
-    const int k = int(i / per_beam);
-    const int64_t j = i - k * per_beam, row = seq * beams + k;
-    BeamKey c{0, ~uint64_t(0)};
-    if (s_state[k] == 1) {
-      const uint64_t key = cand[row * per_beam + j];
-      if (key != 0) {
-        const float x = unorder32(uint32_t(key >> 32));
-        c.total = order64(double(scores[row]) + (double(x) - s_lse[k]));
-        c.place = uint64_t(k) * uint64_t(vocab) + uint32_t(~uint32_t(key));
+  // every candidate of the sequence that this thread looks at
+  auto each = [&](auto &&use) {
+    const int total = beams * per_beam;
+    const uint64_t *p = cand + seq * total;
+    for (int i0 = tid; i0 < total; i0 += 8 * kBeamThreads) {
+      uint64_t key[8];                       // eight loads in flight
+#pragma unroll
+      for (int u = 0; u < 8; ++u) {
+        const int i = i0 + u * kBeamThreads;
+        key[u] = i < total ? p[i] : 0;
       }
-    } else if (s_state[k] == 2 && j == 0) {
-      c.total = order64(double(scores[row]));
-      c.place = uint64_t(k) * uint64_t(vocab) + uint64_t(eos);
+#pragma unroll
+      for (int u = 0; u < 8; ++u) {
+        const uint32_t k = uint32_t(i0 + u * kBeamThreads) / uint32_t(per_beam);
+        if (key[u] != 0 && k < uint32_t(beams) && s_state[k] == 1)
+          use(BeamKey{order64(s_shift[k] + (double(unorder32(uint32_t(key[u] >> 32))) - s_lse[k])),
+                      (k << 24) | ~uint32_t(key[u])});
+      }
     }
-    return c;
+    if (tid < beams && s_state[tid] == 2)
+      use(BeamKey{order64(s_shift[tid]), (uint32_t(tid) << 24) | uint32_t(eos)});
   };
-  BeamKey best{0, ~uint64_t(0)};
-  for (int64_t i = tid; i < total_cand; i += kBeamThreads) {
-    const BeamKey c = candidate(i);
-    if (before(c.total, c.place, best.total, best.place)) best = c;
-  }
-  s_best[tid] = best;
-  if (tid == 0) s_cut = BeamKey{0, ~uint64_t(0)};
+  uint32_t best = 0;      // the leading half of the largest total
+  each([&](const BeamKey &c) {
+    const uint32_t h = uint32_t(c.total >> 32);
+    best = h > best ? h : best;
+  });
+  uint32_t o = __builtin_amdgcn_mov_dpp(int(best), 0xB1, 0xF, 0xF, true);
+  best = o > best ? o : best;
+  o = __builtin_amdgcn_mov_dpp(int(best), 0x4E, 0xF, 0xF, true);
+  best = o > best ? o : best;
+  if ((lane & 3) == 0) s_group[tid >> 2] = best;
   __syncthreads();
-  if (best.total != 0) {
-    int rank = 0;
-    for (int j = 0; j < kBeamThreads; ++j)
-      rank += before(s_best[j].total, s_best[j].place, best.total, best.place) ? 1 : 0;
-    if (rank == n_out - 1) s_cut = best;
-  }
-  __syncthreads();
-  // at least n_out candidates are not behind the cut (all, where there is none)
-  BeamKey cut = s_cut;
-  auto listed = [&](const BeamKey &c) {
-    return c.total != 0 && !before(cut.total, cut.place, c.total, c.place);
-  };
-  for (int64_t i = tid; i < total_cand; i += kBeamThreads) {
-    const BeamKey c = candidate(i);
-    if (listed(c)) {
+  // at least n_out candidates reach the cut (all, where there are fewer groups)
+  const uint32_t cut = wave_cut<32>(s_group[lane], n_out);
+  each([&](const BeamKey &c) {
+    if (uint32_t(c.total >> 32) >= cut) {
       const int at = atomicAdd(&s_count, 1);
-      if (at < kBeamList) s_list[at] = c;
+      if (at < kBeamList) {
+        s_total[at] = c.total;
+        s_place[at] = c.place;
+      }
     }
-  }
+  });
   __syncthreads();
-  int count = s_count;
-  const int64_t o = seq * n_out;
+  const int count = s_count;
+  const int64_t first = seq * n_out;
   auto emit = [&](int at, const BeamKey &c) {
     const bool real = c.total != 0;
-    const int64_t token = real ? int64_t(c.place % uint64_t(vocab)) : -1;
-    out_scores[o + at] = real ? float(unorder64(c.total)) : -INFINITY;
-    out_parents[o + at] = real ? int64_t(c.place / uint64_t(vocab)) : -1;
-    out_tokens[o + at] = token;
-    if (out_finished) out_finished[o + at] = real && token == eos ? 1 : 0;
+    const int64_t token = real ? int64_t(c.place & 0xffffffu) : -1;
+    out_scores[first + at] = real ? float(unorder64(c.total)) : -INFINITY;
+    out_parents[first + at] = real ? int64_t(c.place >> 24) : -1;
+    out_tokens[first + at] = token;
+    if (out_finished) out_finished[first + at] = real && token == eos ? 1 : 0;
   };
   if (count <= kBeamList) {
     for (int i = tid; i < count; i += kBeamThreads) {
-      const BeamKey c = s_list[i];
+      const BeamKey c{s_total[i], s_place[i]};
       int rank = 0;
-      for (int j = 0; j < count; ++j)
-        rank += before(s_list[j].total, s_list[j].place, c.total, c.place) ? 1 : 0;
+      for (int j = 0; j < count; ++j) rank += before(BeamKey{s_total[j], s_place[j]}, c) ? 1 : 0;
       if (rank < n_out) emit(rank, c);
     }
-    for (int i = count + tid; i < n_out; i += kBeamThreads) emit(i, BeamKey{0, ~uint64_t(0)});
+    for (int i = count + tid; i < n_out; i += kBeamThreads) emit(i, BeamKey{0, 0});
     return;
   }
-  // More than the list holds: take the best one n_out times, each after the
-  // one before it.
+  // More than the list holds (totals whose leading halves are equal): take the
+  // best one n_out times, each after the one before it.
   BeamKey last{~uint64_t(0), 0};
   for (int r = 0; r < n_out; ++r) {
-    BeamKey b{0, ~uint64_t(0)};
-    for (int64_t i = tid; i < total_cand; i += kBeamThreads) {
-      const BeamKey c = candidate(i);
-      if (before(last.total, last.place, c.total, c.place) &&
-          before(c.total, c.place, b.total, b.place))
-        b = c;
-    }
+    BeamKey b{0, ~0u};
+    each([&](const BeamKey &c) {
+      if (before(last, c) && before(c, b)) b = c;
+    });
     __syncthreads();
-    s_best[tid] = b;
+    s_total[tid] = b.total;
+    s_place[tid] = b.place;
     __syncthreads();
     for (int half = kBeamThreads / 2; half > 0; half >>= 1) {
-      if (tid < half && before(s_best[tid + half].total, s_best[tid + half].place,
-                               s_best[tid].total, s_best[tid].place))
-        s_best[tid] = s_best[tid + half];
+      if (tid < half) {
+        const BeamKey x{s_total[tid], s_place[tid]}, y{s_total[tid + half], s_place[tid + half]};
+        if (before(y, x)) {
+          s_total[tid] = y.total;
+          s_place[tid] = y.place;
+        }
+      }
       __syncthreads();
     }
-    last = s_best[0];
+    last = BeamKey{s_total[0], s_place[0]};
     if (tid == 0) emit(r, last);
   }
 }
@@ -459,6 +568,7 @@ __global__ void __launch_bounds__(256) beam_reorder_kernel(
 
 struct BeamPlan {
   int64_t rows = 0, pieces = 0;
+  int vecs = 0;             // 8-value vectors a thread of the first kernel holds
   size_t off_stats = 0, off_cand = 0, total = 0;
 };
 
@@ -467,7 +577,10 @@ static int32_t plan_beam(int64_t n_seq, int64_t beams, int64_t vocab, int64_t n_
   if (n_seq > LCE_MAX_N_TOK || beams > kMaxBeams || vocab > LCE_MAX_VOCAB || n_out > kMaxBeamOut)
     return LCE_DIMENSION_TOO_LARGE;
   p->rows = n_seq * beams;
-  p->pieces = ceil_div(vocab, kBeamPiece);
+  // Long pieces leave fewer candidates to merge, short ones spread a small
+  // call over the chip.
+  p->vecs = p->rows * vocab >= int64_t(1024) * kBeamThreads * 64 ? 8 : 2;
+  p->pieces = ceil_div(vocab, kBeamThreads * 8 * p->vecs);
   // (a launch holds fewer than 2^32 threads)
   if (p->rows * p->pieces >= (int64_t(1) << 32) / kBeamThreads) return LCE_WORK_BUDGET_EXCEEDED;
   p->off_stats = 0;
@@ -520,19 +633,22 @@ int32_t lce_beam_select(const lce_tensor *logits, const lce_tensor *scores,
   uint64_t *cand = reinterpret_cast<uint64_t *>(ws + p.off_cand);
   const uint8_t *fin = given(finished) ? static_cast<const uint8_t *>(finished->data) : nullptr;
   const uint8_t *ok = given(allowed) ? static_cast<const uint8_t *>(allowed->data) : nullptr;
-  auto run = [&](auto kernel, auto *x) {
-    kernel<<<uint32_t(p.rows * p.pieces), kBeamThreads, 0, st>>>(x, ok, fin, vocab, int(p.pieces),
-                                                                 int(n_out), cand, stats);
+  auto run = [&](auto type, auto *x) {
+    typedef decltype(type) T;
+    auto go = [&](auto kernel) {
+      kernel<<<uint32_t(p.rows * p.pieces), kBeamThreads, 0, st>>>(
+          x, ok, fin, vocab, int(p.pieces), int(n_out), cand, stats);
+    };
+    if (p.vecs == 8) ok ? go(beam_piece_kernel<T, 8, true>) : go(beam_piece_kernel<T, 8, false>);
+    else ok ? go(beam_piece_kernel<T, 2, true>) : go(beam_piece_kernel<T, 2, false>);
   };
-  if (logits->dtype == LCE_F32)
-    run(beam_piece_kernel<float>, static_cast<const float *>(logits->data));
+  if (logits->dtype == LCE_F32) run(float(), static_cast<const float *>(logits->data));
   else if (logits->dtype == LCE_F16)
-    run(beam_piece_kernel<Half8<true>>, static_cast<const uint16_t *>(logits->data));
-  else
-    run(beam_piece_kernel<Half8<false>>, static_cast<const uint16_t *>(logits->data));
+    run(Half8<true>(), static_cast<const uint16_t *>(logits->data));
+  else run(Half8<false>(), static_cast<const uint16_t *>(logits->data));
   beam_merge_kernel<<<uint32_t(n_seq), kBeamThreads, 0, st>>>(
-      cand, stats, static_cast<const float *>(scores->data), fin, int(beams), vocab,
-      int(p.pieces), int(n_out), eos, static_cast<float *>(out_scores->data),
+      cand, stats, static_cast<const float *>(scores->data), fin, int(beams), int(p.pieces),
+      int(n_out), eos, static_cast<float *>(out_scores->data),
       static_cast<int64_t *>(out_parents->data), static_cast<int64_t *>(out_tokens->data),
       given(out_finished) ? static_cast<uint8_t *>(out_finished->data) : nullptr);
   return enqueued_status();

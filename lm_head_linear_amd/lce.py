@@ -8,7 +8,9 @@ first call raises: there is no fallback path.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
+import functools
 import os
 from dataclasses import dataclass
 from typing import Optional
@@ -211,7 +213,14 @@ def _t(x: Optional[torch.Tensor]) -> Tensor:
     return Tensor(x.data_ptr(), x.numel(), _DT.get(x.dtype, 0))
 
 
+# torch's raw-handle query, where this torch has it: a tenth of the cost of
+# building a Stream object, which short calls would spend most of their time on.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _stream(dev: torch.device) -> int:
+    if _raw_stream is not None and dev.index is not None:
+        return _raw_stream(dev.index)
     return torch.cuda.current_stream(dev).cuda_stream
 
 
@@ -553,6 +562,23 @@ def _on(*tensors) -> torch.device:
     return dev
 
 
+_HERE_ALREADY = contextlib.nullcontext()
+
+
+def _use(dev: torch.device):
+    """Context in which dev is the current device."""
+    return _HERE_ALREADY if torch.cuda.current_device() == dev.index else torch.cuda.device(dev)
+
+
+@functools.lru_cache(maxsize=256)
+def _bytes(query, *shape) -> int:
+    """A workspace query's answer (which depends on its arguments alone)."""
+    n = query(*shape)
+    if n < 0:
+        raise LceError(-n, query.__name__)
+    return n
+
+
 def _check(st: int, where: str):
     if st != OK:
         raise LceError(st, where)
@@ -588,7 +614,7 @@ class Packed8:
 def pack8(x) -> Packed8:
     """Allocate codes and scales, call lce_pack8."""
     n, d = x.shape
-    with torch.cuda.device(_on(x)):
+    with _use(_on(x)):
         codes = torch.empty(n, d, dtype=torch.uint8, device=x.device)
         scales = torch.empty(n, -(-d // PACK8_BLOCK), dtype=torch.uint8, device=x.device)
         _check(lce_pack8(x, n, d, codes, scales), "lce_pack8")
@@ -598,7 +624,7 @@ def pack8(x) -> Packed8:
 def unpack8(packed: Packed8):
     """Allocate the 16-bit tensor, call lce_unpack8."""
     n, d = packed.codes.shape
-    with torch.cuda.device(_on(packed.codes, packed.scales)):
+    with _use(_on(packed.codes, packed.scales)):
         out = torch.empty(n, d, dtype=packed.dtype, device=packed.codes.device)
         _check(lce_unpack8(packed.codes, packed.scales, n, d, out), "lce_unpack8")
     return out
@@ -650,12 +676,11 @@ def beam_select(logits, scores, n_out, finished=None, allowed=None, eos=None, wo
     if rows != n_seq * beams:
         raise ValueError("logits need one row per beam")
     dev = _on(logits, scores, finished, allowed, workspace)
-    with torch.cuda.device(dev):
-        nbytes = lce_beam_workspace_bytes(n_seq, beams, V, n_out)
-        if nbytes < 0:
-            raise LceError(int(-nbytes), "lce_beam_workspace_bytes")
-        ws = workspace if workspace is not None else torch.empty(nbytes, dtype=torch.uint8,
-                                                                 device=dev)
+    with _use(dev):
+        ws = workspace
+        if ws is None:
+            ws = torch.empty(_bytes(lce_beam_workspace_bytes, n_seq, beams, V, n_out),
+                             dtype=torch.uint8, device=dev)
         step = BeamStep(torch.empty(n_seq, n_out, dtype=torch.float32, device=dev),
                         torch.empty(n_seq, n_out, dtype=torch.int64, device=dev),
                         torch.empty(n_seq, n_out, dtype=torch.int64, device=dev),
@@ -692,7 +717,7 @@ def beam_reorder(states, parents, beams, out=None, length=None, dim=2):
         for s in shape[dim:]:
             inner *= s
         elems, stride = length * inner, shape[dim - 1] * inner
-    with torch.cuda.device(_on(parents, *states, *out)):
+    with _use(_on(parents, *states, *out)):
         _check(lce_beam_reorder(states, out, parents, n_seq, beams, n_out, segs, elems, stride),
                "lce_beam_reorder")
     return out
@@ -758,11 +783,9 @@ def linear(x, weight, bias=None, residual=None, activation="none", want_preact=F
             residual is not None and residual.shape != (n, d_out)):
         raise ValueError("weight, bias or residual does not fit x")
     dev = _on(x, weight, bias, residual, workspace)
-    with torch.cuda.device(dev):
+    with _use(dev):
         if workspace is None:
-            nbytes = lce_linear_workspace_bytes(n, d_in, d_out, x.dtype)
-            if nbytes < 0:
-                raise LceError(int(-nbytes), "lce_linear_workspace_bytes")
+            nbytes = _bytes(lce_linear_workspace_bytes, n, d_in, d_out, x.dtype)
             if nbytes > 0:
                 workspace = torch.empty(nbytes, dtype=torch.uint8, device=dev)
         out = torch.empty(n, d_out, dtype=out_dtype or x.dtype, device=dev)
@@ -792,12 +815,11 @@ def linear_backward(d_out, x, weight, preact=None, activation="none", want_x=Tru
     if accumulate and ((want_weight and d_weight is None) or (want_bias and d_bias is None)):
         raise ValueError("accumulate needs the gradients it adds to")
     dev = _on(d_out, x, xs, weight, preact, zs, d_weight, d_bias, workspace)
-    with torch.cuda.device(dev):
+    with _use(dev):
         if workspace is None:
-            nbytes = lce_linear_backward_workspace_bytes(n, d_in, m, d_out.dtype)
-            if nbytes < 0:
-                raise LceError(int(-nbytes), "lce_linear_backward_workspace_bytes")
-            workspace = torch.empty(nbytes, dtype=torch.uint8, device=dev)
+            workspace = torch.empty(
+                _bytes(lce_linear_backward_workspace_bytes, n, d_in, m, d_out.dtype),
+                dtype=torch.uint8, device=dev)
         d_x = torch.empty(n, d_in, dtype=d_out.dtype, device=dev) if want_x else None
         if want_weight and d_weight is None:
             d_weight = torch.empty(m, d_in, dtype=weight_grad_dtype or torch.float32, device=dev)
