@@ -12,8 +12,8 @@
 //
 // Up to 64 tokens run in few_tokens_kernel, which is bound by the read of W;
 // more run on tiles in LDS: the 256 x 256 core of the losses where its tiles
-// fill the chip, else 128 x 128 or 64 x 64 tiles, with the depth split over
-// several tiles where there are few (plan_product).
+// fill the chip, else smaller tiles, with the depth split over several tiles
+// where there are few (plan_product).
 #include <math.h>
 
 #include "ops_gemm.hpp"
@@ -302,9 +302,16 @@ __global__ void __launch_bounds__(256) fold_kernel(const float *part, int64_t ld
 
 // ------------------------------------------------------------------- host --
 
+constexpr int64_t kFewTokens = 64;
+
 // How one product C[m][c], m < M, c < N, depth K runs.
+enum Core {
+  kGeneric,    // register-staged tiles of the losses: any alignment
+  kFew,        // few_tokens_kernel
+  k128x32, k64x64, k128x64, k128x128, k256x256
+};
 struct ProductPlan {
-  int tile = 0;             // 256: the 256 x 256 core, 128, 64: tile_kernel, 0: the generic one
+  Core core = kGeneric;
   int64_t splits = 1, k_per_split = 0;
   size_t part_bytes = 0;    // fp32 partial results of the splits
 };
@@ -314,34 +321,68 @@ struct Operand {
   int64_t ld;
 };
 
-static int64_t tile_count(int64_t M, int64_t N, int t) { return ceil_div(M, t) * ceil_div(N, t); }
+static int64_t tile_count(int64_t M, int64_t N, int64_t bm, int64_t bn) {
+  return ceil_div(M, bm) * ceil_div(N, bn);
+}
 
-// Modelled microseconds of a 64-deep step of one tile on a compute unit that
-// it shares with no other (256) or with what fits beside it (128, 64).
+// Measured on the products alone (M 1024 to 151936, N 32 to 8192, K 512 to
+// 4096, bf16): microseconds of a 64-deep step of one tile alone on a compute
+// unit and with a second one beside it, and what a round of tiles costs
+// besides its steps.  For example 4096 x 2048 x 1024: 36 us with 64 x 64
+// tiles, 27 with 128 x 64, 23 with 128 x 128, 31 with 256 x 256; 1024 x 512 x
+// 1024: 8.5, 10.6, 12.0, 27; 4096 x 4096 x 4096: 231, 167, 133, 109.
+struct TileCost {
+  Core core;
+  int64_t bm, bn;
+  double step_alone, step_shared, round;
+  int64_t at_once;          // tiles the chip runs at a time
+};
+static const TileCost kTiles[] = {
+    {k128x32, 128, 32, 0.28, 0.30, 1.5, 512},   {k64x64, 64, 64, 0.34, 0.41, 2.8, 512},
+    {k128x64, 128, 64, 0.41, 0.62, 3.2, 512},   {k128x128, 128, 128, 0.64, 1.05, 2.5, 512},
+    {k256x256, 256, 256, 1.59, 1.59, 8.0, 256},
+};
+constexpr double kBytesPerUs = 5.0e6;    // what a large copy moves
+
 static ProductPlan plan_product(int64_t M, int64_t N, int64_t K) {
   ProductPlan best;
   double best_us = 1e30;
   const int64_t steps = ceil_div(K, 64);
-  for (const int t : {256, 128, 64}) {
-    const double step_us = t == 256 ? 1.43 : t == 128 ? 0.55 : 0.25;
-    const double fixed_us = t == 256 ? 8.0 : 3.0;
-    const int64_t at_once = t == 256 ? 256 : t == 128 ? 256 : 512;   // tiles running at a time
-    const int64_t tiles = tile_count(M, N, t);
+  const double memory_us = 2.0 * double(K) * double(M + N) / kBytesPerUs;
+  for (const TileCost &t : kTiles) {
+    if (t.core == k128x32 && N > 32) continue;
+    const int64_t tiles = tile_count(M, N, t.bm, t.bn);
     for (int64_t sp = 1; sp <= 16 && sp <= steps; sp *= 2) {
       const int64_t per = ceil_div(steps, sp);
       if ((sp - 1) * per >= steps) continue;
-      const double rounds = double(ceil_div(tiles * sp, at_once));
-      double us = rounds * (fixed_us + per * step_us);
-      if (sp > 1) us += 4.0 + double(M) * double(N) * 4.0 * 2.0 * double(sp) / 4.5e6;
+      const int64_t all = tiles * sp, last = all % t.at_once;
+      double us = double(all / t.at_once) * (t.round + double(per) * t.step_shared);
+      if (last)
+        us += t.round + double(per) * (last <= kComputeUnits ? t.step_alone : t.step_shared);
+      if (us < memory_us) us = memory_us;
+      // the fold: a launch, and the partial results written and read
+      if (sp > 1) us += 3.0 + double(sp) * double(M) * double(N) * 8.0 / kBytesPerUs;
       if (us < best_us) {
         best_us = us;
-        best.tile = t;
+        best.core = t.core;
         best.splits = sp;
         best.k_per_split = per * 64;
       }
     }
   }
   best.part_bytes = best.splits > 1 ? size_t(best.splits * N * round_to(M, 8)) * 4 : 0;
+  // up to 64 rows may stream A instead: bound by the read of A, at a rate that
+  // falls with the rows that share a wave (4.8, 2.9 and 1.9 TB/s measured for
+  // up to 16, 32 and 64 rows of 32768 x 4096), with no ring to fill first
+  if (N <= kFewTokens) {
+    const double floor_us = N <= 16 ? 4.8 : N <= 32 ? 5.7 : 7.5;
+    const double rate = N <= 16 ? 4.8e6 : N <= 32 ? 2.9e6 : 1.9e6;
+    const double us = 2.0 + 2.0 * double(M) * double(K) / rate;
+    if ((us > floor_us ? us : floor_us) < best_us + 2.5) {
+      best = ProductPlan{};
+      best.core = kFew;
+    }
+  }
   return best;
 }
 
@@ -387,7 +428,7 @@ static void run_generic(Operand A, Operand B, int64_t M, int64_t N, int64_t K,
   g.M = M; g.N = N; g.K = K;
   g.k_per_split = round_to(K, TR::BK);
   g.tiles_n = ceil_div(N, TR::BN);
-  const uint32_t tiles = uint32_t(tile_count(M, N, 256));
+  const uint32_t tiles = uint32_t(tile_count(M, N, TR::BM, TR::BN));
   gemm_kernel<TR, AK, BKM, false><<<tiles, TR::NT, 0, st>>>(g, DirectEpi<TR>{out});
 }
 
@@ -406,9 +447,9 @@ static void run_product(const ProductPlan &pl, Operand A, Operand B, int64_t M, 
     o.out_f32 = 1;
     o.split_stride = N * o.ld;
   }
-  if (pl.tile == 0) {
+  if (pl.core == kGeneric) {
     run_generic<F16, AK, BKM>(A, B, M, N, K, out, st);
-  } else if (pl.tile == 256) {
+  } else if (pl.core == k256x256) {
     typedef TraitsH16W8<F16> TR;
     typedef PipeCfg<64, 2> CFG;
     Gemm2Params g = {};
@@ -417,23 +458,23 @@ static void run_product(const ProductPlan &pl, Operand A, Operand B, int64_t M, 
     g.M_read = A.ld; g.N_read = B.ld;
     g.k_per_split = pl.k_per_split;
     g.tiles_n = ceil_div(N, 256);
-    const int64_t wgs = tile_count(M, N, 256) * pl.splits;
-    gemm2_kernel<CFG, TR, AK, BKM, OutEpi<TR>><<<uint32_t(wgs), TR::NT, 0, st>>>(g, OutEpi<TR>{o});
+    const int64_t wgs = tile_count(M, N, 256, 256) * pl.splits;
+    big_kernel<CFG, TR, AK, BKM, OutEpi<TR>><<<uint32_t(wgs), TR::NT, 0, st>>>(g, OutEpi<TR>{o});
   } else if constexpr (AK && BKM) {
     TileParams g = {};
     g.A = A.p; g.lda = A.ld; g.B = B.p; g.ldb = B.ld;
     g.M = M; g.N = N; g.K = K;
     g.k_per_split = pl.k_per_split;
-    g.tiles_n = int32_t(ceil_div(N, pl.tile));
-    g.tiles = int32_t(tile_count(M, N, pl.tile));
-    const uint32_t wgs = uint32_t(g.tiles * pl.splits);
-    if (pl.tile == 128) {
-      typedef Tile<128, 128, 2, 2, 2, F16> T;
-      tile_kernel<T><<<wgs, T::NT, 0, st>>>(g, OutEpi<T>{o});
-    } else {
-      typedef Tile<64, 64, 2, 2, 4, F16> T;
-      tile_kernel<T><<<wgs, T::NT, 0, st>>>(g, OutEpi<T>{o});
-    }
+    auto run = [&](auto tile) {
+      typedef decltype(tile) T;
+      g.tiles_n = int32_t(ceil_div(N, T::BN));
+      g.tiles = int32_t(tile_count(M, N, T::BM, T::BN));
+      tile_kernel<T><<<uint32_t(g.tiles * pl.splits), T::NT, 0, st>>>(g, OutEpi<T>{o});
+    };
+    if (pl.core == k128x32) run(Tile<128, 32, 4, 1, 4, F16>());
+    else if (pl.core == k64x64) run(Tile<64, 64, 2, 2, 4, F16>());
+    else if (pl.core == k128x64) run(Tile<128, 64, 2, 2, 3, F16>());
+    else run(Tile<128, 128, 2, 4, 2, F16>());
   }
   if (pl.splits > 1) {
     const int64_t blocks = ceil_div(o.ld / 8 * out.cols, 256);
@@ -445,10 +486,7 @@ static void run_product(const ProductPlan &pl, Operand A, Operand B, int64_t M, 
 // The tiled cores address 256 rows of an operand with 32-bit byte offsets.
 static bool offsets_fit(int64_t ld) { return 256 * ld * 2 < (int64_t(1) << 31); }
 
-constexpr int64_t kFewTokens = 64;
-
 struct LinearPlan {
-  bool few = false;
   ProductPlan product;
   int64_t ld_in = 0;                      // padded d_in of the copies, 0: no copies
   size_t off_x = 0, off_w = 0, off_part = 0, total = 0;
@@ -462,6 +500,9 @@ struct BackwardPlan {
   size_t off_part = 0, off_sums = 0, total = 0;
 };
 
+// Whether the core takes MN-major operands, as the backward's lie in memory.
+static bool takes_mn(const ProductPlan &p) { return p.core == k256x256 || p.core == kGeneric; }
+
 struct Layout {
   size_t at = 0;
   size_t take(size_t bytes) {
@@ -474,11 +515,11 @@ struct Layout {
 static int32_t plan_linear(int64_t n, int64_t d_in, int64_t d_out, int32_t dtype, LinearPlan *p) {
   if (const int32_t st = lce_dims_check(n, d_in, d_out); st != LCE_OK) return st;
   if (!half_type(dtype)) return LCE_DTYPE_MISMATCH;
-  p->few = n <= kFewTokens;
-  if (p->few) return LCE_OK;
   Layout l;
   p->product = plan_product(d_out, n, d_in);
-  if (d_in % (p->product.tile == 256 ? 64 : 8) != 0) {
+  if (n <= kFewTokens && d_in % 8 != 0) p->product = ProductPlan{kFew};
+  if (p->product.core == kFew) return LCE_OK;
+  if (d_in % (p->product.core == k256x256 ? 64 : 8) != 0) {
     p->ld_in = round_to(d_in, 64);
     p->off_x = l.take(size_t(n * p->ld_in * 2));
     p->off_w = l.take(size_t(d_out * p->ld_in * 2));
@@ -494,17 +535,19 @@ static int32_t plan_linear_backward(int64_t n, int64_t d_in, int64_t d_out, int3
   if (!half_type(dtype)) return LCE_DTYPE_MISMATCH;
   Layout l;
   p->px = plan_product(d_in, n, d_out);
+  if (p->px.core == kFew) p->px = ProductPlan{k64x64, 1, round_to(d_out, 64)};
   p->pw = plan_product(d_in, d_out, n);
+  if (p->pw.core == kFew) p->pw = ProductPlan{k64x64, 1, round_to(n, 64)};
   p->ld_in = round_to(d_in, 64);
   p->ld_out = round_to(d_out, 64);
   p->ld_n = round_to(n, 64);
   if (!offsets_fit(p->ld_out)) p->px = p->pw = ProductPlan{};
-  else if (!offsets_fit(p->ld_n) && p->pw.tile != 256) p->pw = ProductPlan{};
+  else if (!offsets_fit(p->ld_n) && !takes_mn(p->pw)) p->pw = ProductPlan{};
   p->sum_parts = ceil_div(n, 64);
   p->off_g = l.take(size_t(n * p->ld_out * 2));
-  if (p->px.tile == 256 || p->px.tile == 0) p->off_w = l.take(size_t(d_out * p->ld_in * 2));
+  if (takes_mn(p->px)) p->off_w = l.take(size_t(d_out * p->ld_in * 2));
   else p->off_wt = l.take(size_t(d_in * p->ld_out * 2));
-  if (p->pw.tile == 256 || p->pw.tile == 0) {
+  if (takes_mn(p->pw)) {
     p->off_x = l.take(size_t(n * p->ld_in * 2));
   } else {
     p->off_gt = l.take(size_t(d_out * p->ld_n * 2));
@@ -555,11 +598,14 @@ template <bool F16>
 static void linear_run(const LinearPlan &p, const lce_tensor *x, const lce_tensor *w,
                        const OutParams &out, int64_t n, int64_t d_in, int64_t d_out, char *ws,
                        hipStream_t st) {
-  if (p.few) {
+  const bool aligned = aligned_to(x->data, 16) && aligned_to(w->data, 16);
+  if (p.product.core == kFew || (n <= kFewTokens && !aligned)) {
     const int64_t groups = ceil_div(d_out, 16);
-    // waves that share 16 rows: until about 2048 waves run, 128 k each at least
+    // waves that share 16 rows, with 128 k each at least (1024 x 1024, one
+    // token: 7.4, 6.0, 4.8, 4.9 us with 1, 2, 4, 8; 4096 x 4096: 20, 12, 8.3, 8.2)
+    const int most = groups <= 128 ? 8 : 4;
     int kw = 1;
-    while (kw < 8 && groups * kw < 2048 && d_in / (2 * kw) >= 128) kw *= 2;
+    while (kw < most && d_in / (2 * kw) >= 128) kw *= 2;
     const int waves = kw > 4 ? kw : 4, per_block = waves / kw;
     const int64_t k_part = round_to(ceil_div(d_in, kw), 32);
     auto run = [&](auto kernel) {
@@ -586,7 +632,7 @@ static void linear_run(const LinearPlan &p, const lce_tensor *x, const lce_tenso
       *to[i] = {j.dst, p.ld_in};
     }
     run_copies<F16>(jobs, 2, st);
-  } else if (!aligned_to(X.p, 16) || !aligned_to(W.p, 16)) {
+  } else if (!aligned) {
     run_generic<F16, true, true>(W, X, d_out, n, d_in, out, st);
     return;
   }
@@ -613,8 +659,7 @@ static void linear_backward_run(const BackwardPlan &p, const lce_tensor *dy, con
   int count = 0;
   Operand G = {dy->data, d_out}, GT = {nullptr, 0}, X = {nullptr, 0}, W = {nullptr, 0};
   // (the small tiles take transposed copies, the others operands as they lie)
-  const bool small_x = want_x && (p.px.tile == 128 || p.px.tile == 64);
-  const bool small_w = want_w && (p.pw.tile == 128 || p.pw.tile == 64);
+  const bool small_x = want_x && !takes_mn(p.px), small_w = want_w && !takes_mn(p.pw);
   const bool big_x = want_x && !small_x, big_w = want_w && !small_w;
   const bool copy_g = slope || !aligned_to(dy->data, 16) ||
                       (big_x && d_out % 64 != 0) || d_out % 8 != 0;
