@@ -257,15 +257,24 @@ __global__ void __launch_bounds__(256) copies_kernel(CopyJobs jobs) {
   }
 }
 
-// Adds the bias gradient's 64-row sums in order.
+// Adds the bias gradient's 64-row sums: 64 columns a block, a quarter of the
+// rows a wave, each in order.
 template <bool F16>
-__global__ void __launch_bounds__(64) bias_grad_kernel(const float *sums, int64_t parts, int64_t d,
-                                                       void *out, int out_f32, int add) {
-  const int64_t col = int64_t(blockIdx.x) * 64 + threadIdx.x;
-  if (col >= d) return;
+__global__ void __launch_bounds__(256) bias_grad_kernel(const float *sums, int64_t parts, int64_t d,
+                                                        void *out, int out_f32, int add) {
+  __shared__ float s_sum[4][64];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int64_t col = int64_t(blockIdx.x) * 64 + lane;
+  const int64_t per = (parts + 3) / 4, end = (wave + 1) * per < parts ? (wave + 1) * per : parts;
   float s = 0.0f;
+  if (col < d) {
 #pragma unroll 8
-  for (int64_t i = 0; i < parts; ++i) s += sums[i * d + col];
+    for (int64_t i = wave * per; i < end; ++i) s += sums[i * d + col];
+  }
+  s_sum[wave][lane] = s;
+  __syncthreads();
+  if (wave != 0 || col >= d) return;
+  s = ((s_sum[0][lane] + s_sum[1][lane]) + s_sum[2][lane]) + s_sum[3][lane];
   if (out_f32) {
     float *o = static_cast<float *>(out) + col;
     *o = add ? *o + s : s;
@@ -494,14 +503,12 @@ struct LinearPlan {
 
 struct BackwardPlan {
   ProductPlan px, pw;                     // d_x and d_weight
+  bool mn_x = false, mn_w = false;        // operands as they lie, not transposed copies
   int64_t ld_in = 0, ld_out = 0, ld_n = 0;
   int64_t sum_parts = 0;
   size_t off_g = 0, off_gt = 0, off_x = 0, off_xt = 0, off_w = 0, off_wt = 0;
   size_t off_part = 0, off_sums = 0, total = 0;
 };
-
-// Whether the core takes MN-major operands, as the backward's lie in memory.
-static bool takes_mn(const ProductPlan &p) { return p.core == k256x256 || p.core == kGeneric; }
 
 struct Layout {
   size_t at = 0;
@@ -542,12 +549,21 @@ static int32_t plan_linear_backward(int64_t n, int64_t d_in, int64_t d_out, int3
   p->ld_out = round_to(d_out, 64);
   p->ld_n = round_to(n, 64);
   if (!offsets_fit(p->ld_out)) p->px = p->pw = ProductPlan{};
-  else if (!offsets_fit(p->ld_n) && !takes_mn(p->pw)) p->pw = ProductPlan{};
+  else if (!offsets_fit(p->ld_n) && p->pw.core != k256x256) p->pw = ProductPlan{};
+  // Only the 256 x 256 core takes operands that are not K-major.  d_weight's
+  // two are so as they lie and cost it nothing (8192 x 4096 x 4096: 231 us
+  // against 225 K-major); d_x's W beside K-major G costs a fifth (286 us), more
+  // than W's transposed copy unless few tokens share it.
+  const double step_cost = 0.3 * double(ceil_div(tile_count(d_in, n, 256, 256), 256)) *
+                           double(ceil_div(d_out, 64));
+  p->mn_w = p->pw.core == k256x256 || p->pw.core == kGeneric;
+  p->mn_x = p->px.core == kGeneric ||
+            (p->px.core == k256x256 && step_cost < 4.0 * double(d_in) * double(d_out) / kBytesPerUs);
   p->sum_parts = ceil_div(n, 64);
   p->off_g = l.take(size_t(n * p->ld_out * 2));
-  if (takes_mn(p->px)) p->off_w = l.take(size_t(d_out * p->ld_in * 2));
+  if (p->mn_x) p->off_w = l.take(size_t(d_out * p->ld_in * 2));
   else p->off_wt = l.take(size_t(d_in * p->ld_out * 2));
-  if (takes_mn(p->pw)) {
+  if (p->mn_w) {
     p->off_x = l.take(size_t(n * p->ld_in * 2));
   } else {
     p->off_gt = l.take(size_t(d_out * p->ld_n * 2));
@@ -658,11 +674,10 @@ static void linear_backward_run(const BackwardPlan &p, const lce_tensor *dy, con
   CopyJobs jobs = {};
   int count = 0;
   Operand G = {dy->data, d_out}, GT = {nullptr, 0}, X = {nullptr, 0}, W = {nullptr, 0};
-  // (the small tiles take transposed copies, the others operands as they lie)
-  const bool small_x = want_x && !takes_mn(p.px), small_w = want_w && !takes_mn(p.pw);
-  const bool big_x = want_x && !small_x, big_w = want_w && !small_w;
+  const bool kk_x = want_x && !p.mn_x, kk_w = want_w && !p.mn_w;
+  const bool mn_x = want_x && p.mn_x, mn_w = want_w && p.mn_w;
   const bool copy_g = slope || !aligned_to(dy->data, 16) ||
-                      (big_x && d_out % 64 != 0) || d_out % 8 != 0;
+                      (want_x && p.px.core == k256x256 && d_out % 64 != 0) || d_out % 8 != 0;
   {
     CopyJob j = {};
     j.src = dy->data; j.rows = n; j.cols = d_out;
@@ -670,11 +685,11 @@ static void linear_backward_run(const BackwardPlan &p, const lce_tensor *dy, con
       j.z = z->data; j.z_scales = scales_of(z_scales);
       j.act = act;
     }
-    if (copy_g && (want_x || big_w)) {
+    if (copy_g && (want_x || mn_w)) {
       j.dst = at(p.off_g); j.ld = p.ld_out;
       G = {j.dst, j.ld};
     }
-    if (small_w) {
+    if (kk_w) {
       j.dst_t = at(p.off_gt); j.ld_t = p.ld_n;
       GT = {j.dst_t, j.ld_t};
     }
@@ -685,7 +700,7 @@ static void linear_backward_run(const BackwardPlan &p, const lce_tensor *dy, con
     CopyJob j = {};
     j.src = x->data; j.scales = scales_of(x_scales);
     j.rows = n; j.cols = d_in;
-    if (small_w) {
+    if (kk_w) {
       j.dst_t = at(p.off_xt); j.ld_t = p.ld_n;
       X = {j.dst_t, j.ld_t};
     } else if (j.scales || !aligned_to(x->data, 16) || d_in % 8 != 0) {
@@ -699,7 +714,7 @@ static void linear_backward_run(const BackwardPlan &p, const lce_tensor *dy, con
   if (want_x) {
     CopyJob j = {};
     j.src = w->data; j.rows = d_out; j.cols = d_in;
-    if (small_x) {
+    if (kk_x) {
       j.dst_t = at(p.off_wt); j.ld_t = p.ld_out;
       W = {j.dst_t, j.ld_t};
     } else if (!aligned_to(w->data, 16) || d_in % 8 != 0) {
@@ -713,21 +728,23 @@ static void linear_backward_run(const BackwardPlan &p, const lce_tensor *dy, con
   run_copies<F16>(jobs, count, st);
 
   if (want_b)
-    bias_grad_kernel<F16><<<uint32_t(ceil_div(d_out, 64)), 64, 0, st>>>(
+    bias_grad_kernel<F16><<<uint32_t(ceil_div(d_out, 64)), 256, 0, st>>>(
         reinterpret_cast<const float *>(ws + p.off_sums), p.sum_parts, d_out, d_b->data,
         d_b->dtype == LCE_F32, add);
   OutParams o = {};
   if (want_x) {
     o.out = d_x->data; o.ld = d_in; o.rows = d_in; o.cols = n;
-    if (big_x) run_product<F16, false, true>(p.px, W, G, d_in, n, d_out, o, ws + p.off_part, st);
-    else run_product<F16, true, true>(p.px, W, G, d_in, n, round_to(d_out, 8), o, ws + p.off_part, st);
+    if (mn_x) run_product<F16, false, true>(p.px, W, G, d_in, n, d_out, o, ws + p.off_part, st);
+    else run_product<F16, true, true>(p.px, W, G, d_in, n,
+                                      p.px.core == k256x256 ? p.ld_out : round_to(d_out, 8), o,
+                                      ws + p.off_part, st);
   }
   if (want_w) {
     o = {};
     o.out = d_w->data; o.ld = d_in; o.rows = d_in; o.cols = d_out;
     o.out_f32 = d_w->dtype == LCE_F32;
     o.add = add;
-    if (big_w) run_product<F16, false, false>(p.pw, X, G, d_in, d_out, n, o, ws + p.off_part, st);
+    if (mn_w) run_product<F16, false, false>(p.pw, X, G, d_in, d_out, n, o, ws + p.off_part, st);
     else run_product<F16, true, true>(p.pw, X, GT, d_in, d_out, p.ld_n, o, ws + p.off_part, st);
   }
 }

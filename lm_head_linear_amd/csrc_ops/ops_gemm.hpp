@@ -165,6 +165,45 @@ __device__ __forceinline__ void finish(const OutParams &p, float (&z)[W], const 
   }
 }
 
+// The same for eight elements that all exist and overwrite, the residual
+// loaded before.
+template <bool F16>
+__device__ __forceinline__ void finish_whole(const OutParams &p, float (&z)[8], const float (&b)[8],
+                                             const u32x4 &res, int64_t at, int split) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i) z[i] += b[i];
+  if (p.preact) store16(p.preact + at, narrow8<F16>(z));
+  if (p.act == kGelu) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) z[i] = act_value(z[i], kGelu);
+  } else if (p.act == kSilu) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) z[i] = act_value(z[i], kSilu);
+  } else if (p.act == kRelu) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) z[i] = act_value(z[i], kRelu);
+  }
+  if (p.residual) {
+    float r[8];
+    widen8<F16>(res, r);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) z[i] += r[i];
+  }
+  if (p.out_f32) {
+    float *o = static_cast<float *>(p.out) + split * p.split_stride + at;
+    u32x4 x, y;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      x[i] = __float_as_uint(z[i]);
+      y[i] = __float_as_uint(z[4 + i]);
+    }
+    store16(o, x);
+    store16(o + 4, y);
+  } else {
+    store16(static_cast<uint16_t *>(p.out) + at, narrow8<F16>(z));
+  }
+}
+
 // Epilogue of both cores: a wave passes its accumulators through its own part
 // of LDS, 32 rows of the result at a time, so that global accesses are 16
 // bytes a lane along the rows.  The 16-byte chunks of an LDS row are XORed
@@ -189,9 +228,21 @@ struct OutEpi {
     const int count = m >= p.rows ? 0 : (p.rows - m >= 8 ? 8 : int(p.rows - m));
     float b[8];
     load_bias<TR::F16, 8>(p, m, count, b);
+    constexpr int IT = 32 * LPR / 64;                     // rows of a lane in 32 rows
+    const bool whole = mw + TR::WTM <= p.rows && !p.add;  // wave-uniform
 #pragma unroll
     for (int fn = 0; fn < TR::FN; ++fn) {
       const int row = lane & 31;
+      const int64_t c0 = cw + fn * 32 + r0;
+      // the residual's loads go out before the accumulators are moved
+      u32x4 res[IT];
+      if (whole && p.residual) {
+#pragma unroll
+        for (int i = 0; i < IT; ++i) {
+          const int64_t col = c0 + i * (64 / LPR);
+          res[i] = load16(p.residual + (col < p.cols ? col : cw) * p.ld + m);
+        }
+      }
 #pragma unroll
       for (int fm = 0; fm < TR::FM; ++fm)
 #pragma unroll
@@ -203,15 +254,32 @@ struct OutEpi {
           *reinterpret_cast<f32x4 *>(region + row * (TR::WTM * 4) + ((ch ^ (row & MASK)) << 4)) = v;
         }
       asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
-#pragma unroll 1
-      for (int i = 0; i < 32 * LPR / 64; ++i) {
-        const int rr = r0 + i * (64 / LPR);
+      auto sums = [&](int rr, float (&z)[8]) {
         const char *q = region + rr * (TR::WTM * 4);
         const f32x4 a = *reinterpret_cast<const f32x4 *>(q + (((2 * j) ^ (rr & MASK)) << 4));
         const f32x4 c = *reinterpret_cast<const f32x4 *>(q + (((2 * j + 1) ^ (rr & MASK)) << 4));
-        float z[8] = {a[0], a[1], a[2], a[3], c[0], c[1], c[2], c[3]};
-        const int64_t col = cw + fn * 32 + rr;
-        if (col < p.cols && count > 0) finish<TR::F16, 8>(p, z, b, m, col, count, split);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          z[i] = a[i];
+          z[4 + i] = c[i];
+        }
+      };
+      if (whole) {
+#pragma unroll
+        for (int i = 0; i < IT; ++i) {
+          float z[8];
+          sums(r0 + i * (64 / LPR), z);
+          const int64_t col = c0 + i * (64 / LPR);
+          if (col < p.cols) finish_whole<TR::F16>(p, z, b, res[i], col * p.ld + m, split);
+        }
+      } else {
+#pragma unroll 1
+        for (int i = 0; i < IT; ++i) {
+          float z[8];
+          sums(r0 + i * (64 / LPR), z);
+          const int64_t col = c0 + i * (64 / LPR);
+          if (col < p.cols && count > 0) finish<TR::F16, 8>(p, z, b, m, col, count, split);
+        }
       }
       asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");   // read before it is overwritten
     }
