@@ -154,7 +154,7 @@ struct CopyJob {
   uint16_t *dst_t;          // [cols][ld_t], null: none
   int64_t ld_t;
   float *sums;              // [tile rows][cols] sums over 64 rows, null: none
-  int64_t tiles_c, tiles;
+  uint32_t tiles_c, tiles;
   int32_t act;
 };
 constexpr int kMaxCopies = 3;
@@ -189,12 +189,13 @@ template <bool F16>
 __global__ void __launch_bounds__(256) copies_kernel(CopyJobs jobs) {
   __shared__ uint32_t s_t[64 * 33];
   __shared__ float s_sum[4][64];
-  int64_t b = blockIdx.x;
+  uint32_t b = blockIdx.x;
   int which = 0;
   while (which + 1 < kMaxCopies && b >= jobs.job[which].tiles) b -= jobs.job[which++].tiles;
   const CopyJob &j = jobs.job[which];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  const int64_t tr = b / j.tiles_c, r0 = tr * 64, c0 = (b % j.tiles_c) * 64;
+  const uint32_t tile_row = b / j.tiles_c;
+  const int64_t tr = tile_row, r0 = tr * 64, c0 = int64_t(b - tile_row * j.tiles_c) * 64;
   const int cc = tid & 7, pair = tid >> 3;           // 8 columns, rows 2 pair and 2 pair + 1
   const int64_t c = c0 + cc * 8;
   const int count = c >= j.cols ? 0 : (j.cols - c >= 8 ? 8 : int(j.cols - c));
@@ -259,29 +260,60 @@ __global__ void __launch_bounds__(256) copies_kernel(CopyJobs jobs) {
 
 // Adds the bias gradient's 64-row sums: 64 columns a block, a quarter of the
 // rows a wave, each in order.
+struct BiasGrad {
+  const float *sums;       // [parts][d]
+  int64_t parts, d;
+  void *out;
+  int32_t out_f32, add;
+};
 template <bool F16>
-__global__ void __launch_bounds__(256) bias_grad_kernel(const float *sums, int64_t parts, int64_t d,
-                                                        void *out, int out_f32, int add) {
-  __shared__ float s_sum[4][64];
+__device__ inline void bias_grad_block(const BiasGrad &a, uint32_t bid, float *s_sum) {
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int64_t col = int64_t(blockIdx.x) * 64 + lane;
-  const int64_t per = (parts + 3) / 4, end = (wave + 1) * per < parts ? (wave + 1) * per : parts;
-  float s = 0.0f;
-  if (col < d) {
+  const int64_t col = int64_t(bid) * 64 + lane;
+  const int64_t per = (a.parts + 3) / 4, begin = wave * per;
+  const int64_t end = begin + per < a.parts ? begin + per : a.parts;
+  if (wave < 4) {
+    float s = 0.0f;
+    if (col < a.d) {
 #pragma unroll 8
-    for (int64_t i = wave * per; i < end; ++i) s += sums[i * d + col];
+      for (int64_t i = begin; i < end; ++i) s += a.sums[i * a.d + col];
+    }
+    s_sum[wave * 64 + lane] = s;
   }
-  s_sum[wave][lane] = s;
   __syncthreads();
-  if (wave != 0 || col >= d) return;
-  s = ((s_sum[0][lane] + s_sum[1][lane]) + s_sum[2][lane]) + s_sum[3][lane];
-  if (out_f32) {
-    float *o = static_cast<float *>(out) + col;
-    *o = add ? *o + s : s;
+  if (wave != 0 || col >= a.d) return;
+  const float s = ((s_sum[lane] + s_sum[64 + lane]) + s_sum[128 + lane]) + s_sum[192 + lane];
+  if (a.out_f32) {
+    float *o = static_cast<float *>(a.out) + col;
+    *o = a.add ? *o + s : s;
   } else {
-    uint16_t *o = static_cast<uint16_t *>(out) + col;
-    *o = narrow<F16>(add ? widen<F16>(*o) + s : s);
+    uint16_t *o = static_cast<uint16_t *>(a.out) + col;
+    *o = narrow<F16>(a.add ? widen<F16>(*o) + s : s);
   }
+}
+template <bool F16>
+__global__ void __launch_bounds__(256) bias_grad_kernel(BiasGrad a) {
+  __shared__ float s_sum[256];
+  bias_grad_block<F16>(a, blockIdx.x, s_sum);
+}
+
+// The small backward in one launch: two products on the same tiles and the
+// bias gradient's sums, which need nothing of each other.
+template <class T>
+__global__ void __launch_bounds__(T::NT) backward_kernel(TileParams g0, OutEpi<T> e0, TileParams g1,
+                                                         OutEpi<T> e1, BiasGrad bias) {
+  __shared__ __attribute__((aligned(1024))) char smem[T::LDS];
+  uint32_t b = blockIdx.x;
+  if (b < g0.blocks) {
+    tile_block<T>(g0, e0, xcd_order(b, g0.blocks), smem);
+    return;
+  }
+  b -= g0.blocks;
+  if (b < g1.blocks) {
+    tile_block<T>(g1, e1, xcd_order(b, g1.blocks), smem);
+    return;
+  }
+  bias_grad_block<T::F16>(bias, b - g1.blocks, reinterpret_cast<float *>(smem));
 }
 
 // Adds a product's K-splits ([split][cols][ld] fp32) in order and finishes.
@@ -441,6 +473,27 @@ static void run_generic(Operand A, Operand B, int64_t M, int64_t N, int64_t K,
   gemm_kernel<TR, AK, BKM, false><<<tiles, TR::NT, 0, st>>>(g, DirectEpi<TR>{out});
 }
 
+// f(tile type) for one of the K-major tiles.
+template <bool F16, class F>
+static void with_tile(Core core, F &&f) {
+  if (core == k128x32) f(Tile<128, 32, 4, 1, 4, F16>());
+  else if (core == k64x64) f(Tile<64, 64, 2, 2, 4, F16>());
+  else if (core == k128x64) f(Tile<128, 64, 2, 2, 3, F16>());
+  else f(Tile<128, 128, 2, 4, 2, F16>());
+}
+template <class T>
+static TileParams tile_params(const ProductPlan &pl, Operand A, Operand B, int64_t M, int64_t N,
+                              int64_t K) {
+  TileParams g = {};
+  g.A = A.p; g.lda = A.ld; g.B = B.p; g.ldb = B.ld;
+  g.M = M; g.N = N; g.K = K;
+  g.k_per_split = pl.k_per_split;
+  g.tiles_m = uint32_t(ceil_div(M, T::BM));
+  g.tiles_n = uint32_t(ceil_div(N, T::BN));
+  g.blocks = uint32_t(g.tiles_m * g.tiles_n * pl.splits);
+  return g;
+}
+
 // Runs a planned product of padded, aligned operands.  AK, BKM: the operand
 // is K-major (the small tiles take K-major ones only).
 template <bool F16, bool AK, bool BKM>
@@ -470,20 +523,11 @@ static void run_product(const ProductPlan &pl, Operand A, Operand B, int64_t M, 
     const int64_t wgs = tile_count(M, N, 256, 256) * pl.splits;
     big_kernel<CFG, TR, AK, BKM, OutEpi<TR>><<<uint32_t(wgs), TR::NT, 0, st>>>(g, OutEpi<TR>{o});
   } else if constexpr (AK && BKM) {
-    TileParams g = {};
-    g.A = A.p; g.lda = A.ld; g.B = B.p; g.ldb = B.ld;
-    g.M = M; g.N = N; g.K = K;
-    g.k_per_split = pl.k_per_split;
-    auto run = [&](auto tile) {
+    with_tile<F16>(pl.core, [&](auto tile) {
       typedef decltype(tile) T;
-      g.tiles_n = int32_t(ceil_div(N, T::BN));
-      g.tiles = int32_t(tile_count(M, N, T::BM, T::BN));
-      tile_kernel<T><<<uint32_t(g.tiles * pl.splits), T::NT, 0, st>>>(g, OutEpi<T>{o});
-    };
-    if (pl.core == k128x32) run(Tile<128, 32, 4, 1, 4, F16>());
-    else if (pl.core == k64x64) run(Tile<64, 64, 2, 2, 4, F16>());
-    else if (pl.core == k128x64) run(Tile<128, 64, 2, 2, 3, F16>());
-    else run(Tile<128, 128, 2, 4, 2, F16>());
+      const TileParams g = tile_params<T>(pl, A, B, M, N, K);
+      tile_kernel<T><<<g.blocks, T::NT, 0, st>>>(g, OutEpi<T>{o});
+    });
   }
   if (pl.splits > 1) {
     const int64_t blocks = ceil_div(o.ld / 8 * out.cols, 256);
@@ -587,8 +631,8 @@ static void run_copies(CopyJobs &jobs, int count, hipStream_t st) {
     }
     // tiles up to the padded columns of dst and the padded rows of dst_t: the
     // padding ends inside the last tile (multiples of 64)
-    j.tiles_c = ceil_div(j.cols, 64);
-    j.tiles = ceil_div(j.rows, 64) * j.tiles_c;
+    j.tiles_c = uint32_t(ceil_div(j.cols, 64));
+    j.tiles = uint32_t(ceil_div(j.rows, 64)) * j.tiles_c;
     blocks += j.tiles;
   }
   if (blocks) copies_kernel<F16><<<uint32_t(blocks), 256, 0, st>>>(jobs);
@@ -727,26 +771,39 @@ static void linear_backward_run(const BackwardPlan &p, const lce_tensor *dy, con
   }
   run_copies<F16>(jobs, count, st);
 
-  if (want_b)
-    bias_grad_kernel<F16><<<uint32_t(ceil_div(d_out, 64)), 256, 0, st>>>(
-        reinterpret_cast<const float *>(ws + p.off_sums), p.sum_parts, d_out, d_b->data,
-        d_b->dtype == LCE_F32, add);
-  OutParams o = {};
+  const BiasGrad bias = {want_b ? reinterpret_cast<const float *>(ws + p.off_sums) : nullptr,
+                         p.sum_parts, d_out, want_b ? d_b->data : nullptr,
+                         want_b && d_b->dtype == LCE_F32, add};
+  const uint32_t bias_blocks = want_b ? uint32_t(ceil_div(d_out, 64)) : 0;
+  OutParams ox = {}, ow = {};
   if (want_x) {
-    o.out = d_x->data; o.ld = d_in; o.rows = d_in; o.cols = n;
-    if (mn_x) run_product<F16, false, true>(p.px, W, G, d_in, n, d_out, o, ws + p.off_part, st);
-    else run_product<F16, true, true>(p.px, W, G, d_in, n,
-                                      p.px.core == k256x256 ? p.ld_out : round_to(d_out, 8), o,
-                                      ws + p.off_part, st);
+    ox.out = d_x->data; ox.ld = d_in; ox.rows = d_in; ox.cols = n;
   }
   if (want_w) {
-    o = {};
-    o.out = d_w->data; o.ld = d_in; o.rows = d_in; o.cols = d_out;
-    o.out_f32 = d_w->dtype == LCE_F32;
-    o.add = add;
-    if (mn_w) run_product<F16, false, false>(p.pw, X, G, d_in, d_out, n, o, ws + p.off_part, st);
-    else run_product<F16, true, true>(p.pw, X, GT, d_in, d_out, p.ld_n, o, ws + p.off_part, st);
+    ow.out = d_w->data; ow.ld = d_in; ow.rows = d_in; ow.cols = d_out;
+    ow.out_f32 = d_w->dtype == LCE_F32;
+    ow.add = add;
   }
+  const int64_t k_x = p.px.core == k256x256 ? p.ld_out : round_to(d_out, 8);
+  if (kk_x && kk_w && p.px.core == p.pw.core && p.px.core != k256x256 && p.px.splits == 1 &&
+      p.pw.splits == 1) {
+    with_tile<F16>(p.px.core, [&](auto tile) {
+      typedef decltype(tile) T;
+      const TileParams gx = tile_params<T>(p.px, W, G, d_in, n, k_x);
+      const TileParams gw = tile_params<T>(p.pw, X, GT, d_in, d_out, p.ld_n);
+      // (the deeper product first: its tiles take longest)
+      const bool w_first = p.ld_n > k_x;
+      backward_kernel<T><<<gx.blocks + gw.blocks + bias_blocks, T::NT, 0, st>>>(
+          w_first ? gw : gx, OutEpi<T>{w_first ? ow : ox}, w_first ? gx : gw,
+          OutEpi<T>{w_first ? ox : ow}, bias);
+    });
+    return;
+  }
+  if (want_b) bias_grad_kernel<F16><<<bias_blocks, 256, 0, st>>>(bias);
+  if (mn_x) run_product<F16, false, true>(p.px, W, G, d_in, n, d_out, ox, ws + p.off_part, st);
+  if (kk_x) run_product<F16, true, true>(p.px, W, G, d_in, n, k_x, ox, ws + p.off_part, st);
+  if (mn_w) run_product<F16, false, false>(p.pw, X, G, d_in, d_out, n, ow, ws + p.off_part, st);
+  if (kk_w) run_product<F16, true, true>(p.pw, X, GT, d_in, d_out, p.ld_n, ow, ws + p.off_part, st);
 }
 
 }  // namespace lce

@@ -308,7 +308,8 @@ struct TileParams {
   int64_t lda, ldb;          // elements
   int64_t M, N, K;           // K a multiple of 8
   int64_t k_per_split;       // multiple of 64
-  int32_t tiles_n, tiles;    // tiles of one split
+  uint32_t tiles_m, tiles_n; // of one split
+  uint32_t blocks;           // tiles x splits
 };
 
 // ROWS rows of one operand.
@@ -349,38 +350,45 @@ struct TileOperand {
 // that an XCD works on at a time (neighbours in this order) form a patch that
 // shares operand rows in its L2, where a plain row-by-row order reads one
 // operand once per tile.
-constexpr int64_t kGroupM = 4;
-__device__ inline void tile_at(int64_t L, int64_t tiles_m, int64_t tiles_n, int64_t &m, int64_t &n) {
-  const int64_t per_group = kGroupM * tiles_n, g = L / per_group, r = L - g * per_group;
-  const int64_t first = g * kGroupM;
-  const int64_t rows = tiles_m - first < kGroupM ? tiles_m - first : kGroupM;
+constexpr uint32_t kGroupM = 4;
+__device__ inline void tile_at(uint32_t L, uint32_t tiles_m, uint32_t tiles_n, uint32_t &m,
+                               uint32_t &n) {
+  const uint32_t per_group = kGroupM * tiles_n, g = L / per_group, r = L - g * per_group;
+  const uint32_t first = g * kGroupM;
+  const uint32_t rows = tiles_m - first < kGroupM ? tiles_m - first : kGroupM;
   n = r / rows;
   m = first + (r - n * rows);
+}
+// xcd_remap for grids below 2^32 (a 64-bit division costs a small kernel a
+// good part of its time).
+__device__ inline uint32_t xcd_order(uint32_t b, uint32_t nb) {
+  const uint32_t xcd = b % 8, idx = b / 8, q = nb / 8, r = nb % 8;
+  return xcd < r ? xcd * (q + 1) + idx : r * (q + 1) + (xcd - r) * q + idx;
 }
 
 // The 256 x 256 core in that order.
 template <class CFG, class TR, bool AK, bool BKM, class Epi>
 __global__ void __launch_bounds__(TR::NT) big_kernel(Gemm2Params g, Epi epi) {
   __shared__ __attribute__((aligned(1024))) char smem[gemm2_lds_bytes<CFG, Epi>()];
-  const int64_t LS = xcd_remap(blockIdx.x, gridDim.x);
-  const int64_t tiles_m = (g.M + CFG::BM - 1) / CFG::BM, tiles = tiles_m * g.tiles_n;
-  const int64_t split = LS / tiles;
-  int64_t m, n;
-  tile_at(LS - split * tiles, tiles_m, g.tiles_n, m, n);
-  gemm2_tile<CFG, TR, AK, BKM, Epi>(g, epi, split * tiles + m * g.tiles_n + n, smem);
+  const uint32_t LS = xcd_order(blockIdx.x, gridDim.x);
+  const uint32_t tiles_m = uint32_t((g.M + CFG::BM - 1) / CFG::BM), tiles_n = uint32_t(g.tiles_n);
+  const uint32_t tiles = tiles_m * tiles_n, split = LS / tiles;
+  uint32_t m, n;
+  tile_at(LS - split * tiles, tiles_m, tiles_n, m, n);
+  gemm2_tile<CFG, TR, AK, BKM, Epi>(g, epi, int64_t(split * tiles + m * tiles_n + n), smem);
 }
 
-// One tile of one split; `bid` of `tiles * splits` workgroups.
+// One tile of one split; `bid` of `blocks` workgroups.
 template <class T, class Epi>
-__device__ __forceinline__ void tile_block(const TileParams &g, const Epi &epi, int64_t bid,
+__device__ __forceinline__ void tile_block(const TileParams &g, const Epi &epi, uint32_t bid,
                                            char *smem) {
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wm = wave / T::WAVES_N, wn = wave % T::WAVES_N;
-  const int split = int(bid / g.tiles), t = int(bid % g.tiles);
-  int64_t tm, tn;
-  tile_at(t, g.tiles / g.tiles_n, g.tiles_n, tm, tn);
-  const int64_t m0 = tm * T::BM, n0 = tn * T::BN;
+  const uint32_t tiles = g.tiles_m * g.tiles_n, split = bid / tiles;
+  uint32_t tm, tn;
+  tile_at(bid - split * tiles, g.tiles_m, g.tiles_n, tm, tn);
+  const int64_t m0 = int64_t(tm) * T::BM, n0 = int64_t(tn) * T::BN;
   const int64_t kb = split * g.k_per_split;
   const int64_t ke = kb + g.k_per_split < g.K ? kb + g.k_per_split : g.K;
   const int n_k = ke > kb ? int((ke - kb + 63) / 64) : 0;
@@ -418,29 +426,35 @@ __device__ __forceinline__ void tile_block(const TileParams &g, const Epi &epi, 
     wait_vm_barrier_stages<LPS, T::STAGES - 2>(n_k - 1 - it);
     if (it + T::STAGES - 1 < n_k) issue(it + T::STAGES - 1);
     const char *sa = smem + (it % T::STAGES) * T::STAGE_BYTES, *sb = sa + T::BM * 128;
+    // The reads of the whole stage go out together: with one wave a SIMD each
+    // substep would otherwise wait for its own.
+    u32x4 fa[4][T::FM], fb[4][T::FN];
 #pragma unroll
     for (int kk = 0; kk < 4; ++kk) {
-      u32x4 fa[T::FM], fb[T::FN];
 #pragma unroll
       for (int a = 0; a < T::FM; ++a)
-        fa[a] = TileOperand<T, T::BM>::frag(sa, wm * T::WTM + a * 32, kk, lane);
+        fa[kk][a] = TileOperand<T, T::BM>::frag(sa, wm * T::WTM + a * 32, kk, lane);
 #pragma unroll
       for (int b = 0; b < T::FN; ++b)
-        fb[b] = TileOperand<T, T::BN>::frag(sb, wn * T::WTN + b * 32, kk, lane);
+        fb[kk][b] = TileOperand<T, T::BN>::frag(sb, wn * T::WTN + b * 32, kk, lane);
+    }
+#pragma unroll
+    for (int kk = 0; kk < 4; ++kk)
 #pragma unroll
       for (int a = 0; a < T::FM; ++a)
 #pragma unroll
-        for (int b = 0; b < T::FN; ++b) acc[a][b] = mfma32<T>(fa[a], fb[b], acc[a][b]);
-    }
+        for (int b = 0; b < T::FN; ++b) acc[a][b] = mfma32<T>(fa[kk][a], fb[kk][b], acc[a][b]);
+    __builtin_amdgcn_sched_group_barrier(0x100, 4 * (T::FM + T::FN), 0);
+    __builtin_amdgcn_sched_group_barrier(0x008, 4 * T::FM * T::FN, 0);
   }
   __syncthreads();     // the ring becomes the epilogue's staging space
-  epi.staged(acc, m0, n0, wm, wn, lane, split, smem, nullptr);
+  epi.staged(acc, m0, n0, wm, wn, lane, int(split), smem, nullptr);
 }
 
 template <class T, class Epi>
 __global__ void __launch_bounds__(T::NT) tile_kernel(TileParams g, Epi epi) {
   __shared__ __attribute__((aligned(1024))) char smem[T::LDS];
-  tile_block<T>(g, epi, xcd_remap(blockIdx.x, gridDim.x), smem);
+  tile_block<T>(g, epi, xcd_order(blockIdx.x, g.blocks), smem);
 }
 
 }  // namespace lce
