@@ -16,6 +16,8 @@
 // where there are few (plan_product).
 #include <math.h>
 
+#include <numeric>
+
 #include "ops_gemm.hpp"
 
 namespace lce {
@@ -158,38 +160,72 @@ struct CopyJob {
   int32_t act;
 };
 constexpr int kMaxCopies = 3;
+constexpr uint32_t kCopyRun = 64;
 struct CopyJobs {
   CopyJob job[kMaxCopies];
+  uint32_t stride;          // of the runs' order, prime to their number; 1: as they come
 };
 
-// Eight saved values from column c of a row on, `count` of them.
-template <bool F16>
-__device__ inline void saved8(const void *v, const uint8_t *scales, int64_t row, int64_t cols,
-                              int64_t c, int count, float (&f)[8]) {
+// Eight saved values from column c of a row on, `count` of them: as they lie
+// in memory (loads of several may be in flight), then as fp32.
+struct Raw8 {
+  u32x4 v;
+  int scale;
+};
+__device__ inline Raw8 load_saved(const void *v, const uint8_t *scales, int64_t row, int64_t cols,
+                                  int64_t c, int count) {
+  Raw8 r = {u32x4{0, 0, 0, 0}, 127};
   if (!scales) {
-    read_half<F16, 8>(static_cast<const uint16_t *>(v) + row * cols + c, count, f);
-    return;
+    const uint16_t *p = static_cast<const uint16_t *>(v) + row * cols + c;
+    if (count == 8) {
+      r.v = load16(p);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        if (i < count) r.v[i >> 1] |= uint32_t(p[i]) << (16 * (i & 1));
+    }
+    return r;
   }
   const uint8_t *p = static_cast<const uint8_t *>(v) + row * cols + c;
-  uint32_t q[2] = {0, 0};
+  // (eight columns from a multiple of 8 on share a block of 32)
+  r.scale = scales[row * ((cols + 31) / 32) + c / 32];
   if (count == 8) {
-    __builtin_memcpy(q, p, 8);
+    const AnyVec8 q = *reinterpret_cast<const AnyVec8 *>(p);
+    r.v[0] = q.v[0];
+    r.v[1] = q.v[1];
   } else {
 #pragma unroll
     for (int i = 0; i < 8; ++i)
-      if (i < count) q[i >> 2] |= uint32_t(p[i]) << (8 * (i & 3));
+      if (i < count) r.v[i >> 2] |= uint32_t(p[i]) << (8 * (i & 3));
   }
-  // (eight columns from a multiple of 8 on share a block of 32)
-  codes_to_f32(q[0], q[1], int(scales[row * ((cols + 31) / 32) + c / 32]) - 127, f);
+  return r;
+}
+template <bool F16>
+__device__ inline void saved_values(const Raw8 &r, bool codes, float (&f)[8]) {
+  if (!codes) {
+    widen8<F16>(r.v, f);
+    return;
+  }
+  codes_to_f32(r.v[0], r.v[1], r.scale - 127, f);
+  // exact in the 16-bit type but where the largest codes pass its range
+  if (r.scale >= 127 + (F16 ? 8 : 119) || r.scale < 127 + (F16 ? -15 : -117)) {
 #pragma unroll
-  for (int i = 0; i < 8; ++i) f[i] = widen<F16>(saturate16<F16>(f[i]));
+    for (int i = 0; i < 8; ++i) f[i] = widen<F16>(saturate16<F16>(f[i]));
+  }
 }
 
 template <bool F16>
 __global__ void __launch_bounds__(256) copies_kernel(CopyJobs jobs) {
   __shared__ uint32_t s_t[64 * 33];
-  __shared__ float s_sum[4][64];
+  __shared__ float s_sum[4 * 64];
+  // The jobs' blocks are mixed (some compute much, some move much), in runs of
+  // kCopyRun neighbours of a job.
+  const uint32_t runs = gridDim.x / kCopyRun;
   uint32_t b = blockIdx.x;
+  if (jobs.stride > 1 && b < runs * kCopyRun) {
+    const uint32_t run = b / kCopyRun;
+    b = uint32_t(uint64_t(run) * jobs.stride % runs) * kCopyRun + b % kCopyRun;
+  }
   int which = 0;
   while (which + 1 < kMaxCopies && b >= jobs.job[which].tiles) b -= jobs.job[which++].tiles;
   const CopyJob &j = jobs.job[which];
@@ -201,17 +237,28 @@ __global__ void __launch_bounds__(256) copies_kernel(CopyJobs jobs) {
   const int count = c >= j.cols ? 0 : (j.cols - c >= 8 ? 8 : int(j.cols - c));
   float sum[8] = {0, 0, 0, 0, 0, 0, 0, 0};
   u32x4 v[2] = {u32x4{0, 0, 0, 0}, u32x4{0, 0, 0, 0}};
+  Raw8 x[2] = {}, z[2] = {};
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {           // all loads before the first use
+    const int64_t row = r0 + 2 * pair + h;
+    if (row < j.rows && count > 0) {
+      x[h] = load_saved(j.src, j.scales, row, j.cols, c, count);
+      if (j.z) z[h] = load_saved(j.z, j.z_scales, row, j.cols, c, count);
+    }
+  }
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
     const int64_t row = r0 + 2 * pair + h;
-    if (row < j.rows && count > 0) {
+    if (!j.z && !j.sums && !j.scales) {
+      v[h] = x[h].v;                      // moved as it is
+    } else if (row < j.rows && count > 0) {
       float f[8];
-      saved8<F16>(j.src, j.scales, row, j.cols, c, count, f);
+      saved_values<F16>(x[h], j.scales != nullptr, f);
       if (j.z) {
-        float z[8];
-        saved8<F16>(j.z, j.z_scales, row, j.cols, c, count, z);
+        float g[8];
+        saved_values<F16>(z[h], j.z_scales != nullptr, g);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) f[i] *= act_slope(z[i], j.act);
+        for (int i = 0; i < 8; ++i) f[i] *= act_slope(g[i], j.act);
       }
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
@@ -236,14 +283,14 @@ __global__ void __launch_bounds__(256) copies_kernel(CopyJobs jobs) {
     for (int i = 0; i < 8; ++i) {
 #pragma unroll
       for (int o = 8; o < 64; o <<= 1) sum[i] += __shfl_xor(sum[i], o);
-      if (lane < 8) s_sum[wave][cc * 8 + i] = sum[i];
+      if (lane < 8) s_sum[wave * 64 + cc * 8 + i] = sum[i];
     }
   }
   if (!j.dst_t && !j.sums) return;      // block-uniform
   __syncthreads();
   if (j.sums && tid < 64 && c0 + tid < j.cols)
     j.sums[tr * j.cols + c0 + tid] =
-        ((s_sum[0][tid] + s_sum[1][tid]) + s_sum[2][tid]) + s_sum[3][tid];
+        ((s_sum[tid] + s_sum[64 + tid]) + s_sum[128 + tid]) + s_sum[192 + tid];
   if (j.dst_t) {
     const int col = tid >> 2, q = tid & 3;
     const int64_t t0 = r0 + q * 16;
@@ -496,9 +543,11 @@ static TileParams tile_params(const ProductPlan &pl, Operand A, Operand B, int64
 
 // Runs a planned product of padded, aligned operands.  AK, BKM: the operand
 // is K-major (the small tiles take K-major ones only).
+// `any`: K-major operands at any alignment (not for the 256 x 256 core).
 template <bool F16, bool AK, bool BKM>
 static void run_product(const ProductPlan &pl, Operand A, Operand B, int64_t M, int64_t N,
-                        int64_t K, const OutParams &out, char *part, hipStream_t st) {
+                        int64_t K, const OutParams &out, char *part, hipStream_t st,
+                        bool any = false) {
   OutParams o = out;
   if (pl.splits > 1) {
     o = {};
@@ -526,7 +575,8 @@ static void run_product(const ProductPlan &pl, Operand A, Operand B, int64_t M, 
     with_tile<F16>(pl.core, [&](auto tile) {
       typedef decltype(tile) T;
       const TileParams g = tile_params<T>(pl, A, B, M, N, K);
-      tile_kernel<T><<<g.blocks, T::NT, 0, st>>>(g, OutEpi<T>{o});
+      if (any) any_tile_kernel<T><<<g.blocks, T::NT, 0, st>>>(g, OutEpi<T>{o});
+      else tile_kernel<T><<<g.blocks, T::NT, 0, st>>>(g, OutEpi<T>{o});
     });
   }
   if (pl.splits > 1) {
@@ -542,6 +592,7 @@ static bool offsets_fit(int64_t ld) { return 256 * ld * 2 < (int64_t(1) << 31); 
 struct LinearPlan {
   ProductPlan product;
   int64_t ld_in = 0;                      // padded d_in of the copies, 0: no copies
+  bool any = false;                       // rows that are not aligned are read as they lie
   size_t off_x = 0, off_w = 0, off_part = 0, total = 0;
 };
 
@@ -570,7 +621,21 @@ static int32_t plan_linear(int64_t n, int64_t d_in, int64_t d_out, int32_t dtype
   p->product = plan_product(d_out, n, d_in);
   if (n <= kFewTokens && d_in % 8 != 0) p->product = ProductPlan{kFew};
   if (p->product.core == kFew) return LCE_OK;
-  if (d_in % (p->product.core == k256x256 ? 64 : 8) != 0) {
+  if (p->product.core == k256x256 ? d_in % 64 != 0 : d_in % 8 != 0) {
+    // Odd rows: read as they lie, where a step of a tile costs more (vector
+    // loads off a 16-byte boundary), or from padded copies (a launch, and both
+    // operands read and written).  515 x 1003 -> 777 fp16: 11.7 us against
+    // 13.3; 777 x 1003 -> 1531: 16.7 either way; larger ones gain from copies.
+    for (const TileCost &t : kTiles) {
+      if (t.core != p->product.core || t.core == k256x256) continue;
+      const int64_t all = tile_count(d_out, n, t.bm, t.bn) * p->product.splits;
+      const double rounds = double(ceil_div(all, t.at_once)) * (all <= kComputeUnits ? 1.0 : 2.0);
+      const double slower = 0.1 * double(t.bm + t.bn) / 64.0 * rounds *
+                            double(p->product.k_per_split / 64);
+      p->any = slower < 4.0 + 4.0 * double(d_in) * double(n + d_out) / kBytesPerUs;
+    }
+  }
+  if (!p->any && (p->product.core == k256x256 ? d_in % 64 != 0 : d_in % 8 != 0)) {
     p->ld_in = round_to(d_in, 64);
     p->off_x = l.take(size_t(n * p->ld_in * 2));
     p->off_w = l.take(size_t(d_out * p->ld_in * 2));
@@ -635,6 +700,12 @@ static void run_copies(CopyJobs &jobs, int count, hipStream_t st) {
     j.tiles = uint32_t(ceil_div(j.rows, 64)) * j.tiles_c;
     blocks += j.tiles;
   }
+  jobs.stride = 1;
+  const uint32_t runs = uint32_t(blocks) / kCopyRun;
+  if (count > 1 && runs > 8) {
+    jobs.stride = runs * 5 / 8;                  // far apart, any job next to any other
+    while (std::gcd(jobs.stride, runs) != 1) ++jobs.stride;
+  }
   if (blocks) copies_kernel<F16><<<uint32_t(blocks), 256, 0, st>>>(jobs);
 }
 
@@ -692,12 +763,13 @@ static void linear_run(const LinearPlan &p, const lce_tensor *x, const lce_tenso
       *to[i] = {j.dst, p.ld_in};
     }
     run_copies<F16>(jobs, 2, st);
-  } else if (!aligned) {
+  } else if (!aligned && p.product.core == k256x256) {
     run_generic<F16, true, true>(W, X, d_out, n, d_in, out, st);
     return;
   }
+  const bool any = !p.ld_in && (!aligned || p.any);
   run_product<F16, true, true>(p.product, W, X, d_out, n, p.ld_in ? p.ld_in : d_in, out,
-                               ws + p.off_part, st);
+                               ws + p.off_part, st, any);
 }
 
 template <bool F16>

@@ -457,4 +457,123 @@ __global__ void __launch_bounds__(T::NT) tile_kernel(TileParams g, Epi epi) {
   tile_block<T>(g, epi, xcd_order(blockIdx.x, g.blocks), smem);
 }
 
+// The same tile of operands at any alignment: vector loads to registers, two
+// or four stages ahead, and from there to LDS (the DMA needs aligned rows, so it would
+// take a padded copy of both operands first: 777 x 1003 -> 1531 fp16 17.7 us
+// with copies).
+template <class T, int ROWS>
+struct AnyOperand {
+  static constexpr int N = ROWS * 8 / T::NT;      // 16-byte chunks per thread
+  const uint16_t *p[N];
+  int at[N], kc[N];
+  __device__ inline void init(const void *base, int64_t ld, int64_t row0, int64_t rows, int tid) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const int u = tid + i * T::NT, r = u >> 3, c = u & 7;
+      const int64_t row = row0 + r < rows ? row0 + r : rows - 1;   // rows behind the last: unused
+      p[i] = static_cast<const uint16_t *>(base) + row * ld + c * 8;
+      kc[i] = c * 8;
+      at[i] = r * 128 + ((c ^ kswz<128>(r)) << 4);
+    }
+  }
+  __device__ inline void load(int64_t k0, int64_t k_end, u32x4 (&reg)[N]) const {
+    if (k0 + 64 <= k_end) {
+#pragma unroll
+      for (int i = 0; i < N; ++i) reg[i] = load16(p[i] + k0);
+    } else {
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        const int64_t left = k_end - k0 - kc[i];
+        u32x4 v = {0, 0, 0, 0};
+        if (left >= 8) {
+          v = load16(p[i] + k0);
+        } else {
+#pragma unroll
+          for (int e = 0; e < 8; ++e)
+            if (e < left) v[e >> 1] |= uint32_t(p[i][k0 + e]) << (16 * (e & 1));
+        }
+        reg[i] = v;
+      }
+    }
+  }
+  __device__ inline void store(const u32x4 (&reg)[N], char *dst) const {
+#pragma unroll
+    for (int i = 0; i < N; ++i) *reinterpret_cast<u32x4 *>(dst + at[i]) = reg[i];
+  }
+};
+
+template <class T, class Epi>
+__global__ void __launch_bounds__(T::NT) any_tile_kernel(TileParams g, Epi epi) {
+  // stages in flight, as far as 64 registers hold them
+  constexpr int DEPTH = (T::BM + T::BN) * 8 / T::NT <= 4 ? 4 : 2;
+  constexpr int RING = 2 * T::STAGE_BYTES;
+  __shared__ __attribute__((aligned(1024))) char smem[RING > T::EPI ? RING : T::EPI];
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int wm = wave / T::WAVES_N, wn = wave % T::WAVES_N;
+  const uint32_t bid = xcd_order(blockIdx.x, g.blocks);
+  const uint32_t tiles = g.tiles_m * g.tiles_n, split = bid / tiles;
+  uint32_t tm, tn;
+  tile_at(bid - split * tiles, g.tiles_m, g.tiles_n, tm, tn);
+  const int64_t m0 = int64_t(tm) * T::BM, n0 = int64_t(tn) * T::BN;
+  const int64_t kb = split * g.k_per_split;
+  const int64_t ke = kb + g.k_per_split < g.K ? kb + g.k_per_split : g.K;
+  const int n_k = ke > kb ? int((ke - kb + 63) / 64) : 0;
+
+  AnyOperand<T, T::BM> oa;
+  AnyOperand<T, T::BN> ob;
+  oa.init(g.A, g.lda, m0, g.M, tid);
+  ob.init(g.B, g.ldb, n0, g.N, tid);
+  u32x4 ra[DEPTH][AnyOperand<T, T::BM>::N], rb[DEPTH][AnyOperand<T, T::BN>::N];
+  f32x16 acc[T::FM][T::FN];
+#pragma unroll
+  for (int a = 0; a < T::FM; ++a)
+#pragma unroll
+    for (int b = 0; b < T::FN; ++b)
+#pragma unroll
+      for (int r = 0; r < 16; ++r) acc[a][b][r] = 0.0f;
+
+#pragma unroll
+  for (int s = 0; s < DEPTH; ++s)
+    if (s < n_k) {
+      oa.load(kb + s * 64, ke, ra[s]);
+      ob.load(kb + s * 64, ke, rb[s]);
+    }
+  for (int it0 = 0; it0 < n_k; it0 += DEPTH) {
+#pragma unroll
+    for (int h = 0; h < DEPTH; ++h) {
+      const int it = it0 + h;
+      if (it < n_k) {                                   // uniform
+        char *sa = smem + (h & 1) * T::STAGE_BYTES, *sb = sa + T::BM * 128;
+        // (stage it - 2, in this buffer, was read before the last barrier)
+        oa.store(ra[h], sa);
+        ob.store(rb[h], sb);
+        __syncthreads();
+        if (it + DEPTH < n_k) {
+          oa.load(kb + int64_t(it + DEPTH) * 64, ke, ra[h]);
+          ob.load(kb + int64_t(it + DEPTH) * 64, ke, rb[h]);
+        }
+        u32x4 fa[4][T::FM], fb[4][T::FN];
+#pragma unroll
+        for (int kk = 0; kk < 4; ++kk) {
+#pragma unroll
+          for (int a = 0; a < T::FM; ++a)
+            fa[kk][a] = TileOperand<T, T::BM>::frag(sa, wm * T::WTM + a * 32, kk, lane);
+#pragma unroll
+          for (int b = 0; b < T::FN; ++b)
+            fb[kk][b] = TileOperand<T, T::BN>::frag(sb, wn * T::WTN + b * 32, kk, lane);
+        }
+#pragma unroll
+        for (int kk = 0; kk < 4; ++kk)
+#pragma unroll
+          for (int a = 0; a < T::FM; ++a)
+#pragma unroll
+            for (int b = 0; b < T::FN; ++b) acc[a][b] = mfma32<T>(fa[kk][a], fb[kk][b], acc[a][b]);
+      }
+    }
+  }
+  __syncthreads();
+  epi.staged(acc, m0, n0, wm, wn, lane, int(split), smem, nullptr);
+}
+
 }  // namespace lce

@@ -141,7 +141,8 @@ def test_some_gradients_only():
                             want_bias=True)
     assert torch.equal(a.d_x, full.d_x) and a.d_weight is None and a.d_bias is None
     assert torch.equal(b.d_weight, full.d_weight) and b.d_x is None
-    assert torch.equal(c.d_bias, full.d_bias) and c.d_x is None and c.d_weight is None
+    assert c.d_x is None and c.d_weight is None       # (its sums may run in another order)
+    _check_backward(dy, x, w, z, "gelu", c)
 
 
 @pytest.mark.parametrize("wdt", ["f32", "bf16"])
