@@ -1,34 +1,33 @@
-"""Plain 64-bit numpy forms of the operators next to the losses."""
+"""Plain 64-bit forms of the operators next to the losses: torch float64 for
+the linear layer (on whatever device its inputs are), numpy for the others."""
 import math
 
 import numpy as np
+import torch
 
 ACTS = ("none", "relu", "gelu", "silu")
 
 
-def erf(x):
-    return np.vectorize(math.erf, otypes=[np.float64])(x)
-
-
 def act(z, name):
     if name == "relu":
-        return np.maximum(z, 0.0)
+        return z.clamp(min=0.0)
     if name == "gelu":
-        return 0.5 * z * (1.0 + erf(z / math.sqrt(2.0)))
+        return 0.5 * z * (1.0 + torch.erf(z / math.sqrt(2.0)))
     if name == "silu":
-        return z / (1.0 + np.exp(-z))
+        return z / (1.0 + torch.exp(-z))
     return z
 
 
 def act_slope(z, name):
     if name == "relu":
-        return (z > 0).astype(np.float64)
+        return (z > 0).double()
     if name == "gelu":
-        return 0.5 * (1.0 + erf(z / math.sqrt(2.0))) + z * np.exp(-0.5 * z * z) / math.sqrt(2 * math.pi)
+        return (0.5 * (1.0 + torch.erf(z / math.sqrt(2.0)))
+                + z * torch.exp(-0.5 * z * z) / math.sqrt(2 * math.pi))
     if name == "silu":
-        s = 1.0 / (1.0 + np.exp(-z))
+        s = 1.0 / (1.0 + torch.exp(-z))
         return s * (1.0 + z * (1.0 - s))
-    return np.ones_like(z)
+    return torch.ones_like(z)
 
 
 def linear(x, w, b=None, r=None, name="none"):

@@ -10,7 +10,6 @@ half a step, eps/2 relatively, or for fp16 2^-25 absolutely; an fp32 result
 2^-24.  In the backward g = dy act'(z): the slope errs by at most
 2^-20 max(1, |z|) and g is rounded to 16 bits once, so a product with g errs by
 the sum over |g's error| |b| besides its own summation."""
-import numpy as np
 import pytest
 import torch
 
@@ -34,16 +33,19 @@ def _half(dt):
 def _round(y, err, dt):
     """The error of rounding a value that is y but for err to dt."""
     if dt == torch.float32:
-        return err + 2.0 ** -24 * (np.abs(y) + err)
+        return err + 2.0 ** -24 * (y.abs() + err)
     rel, small = _half(dt)
-    return err + rel * (np.abs(y) + err) + small
+    return err + rel * (y.abs() + err) + small
 
 
 def _within(got, want, tol):
-    got = got.double().cpu().numpy()
-    bad = ~(np.abs(got - want) <= tol)
-    assert not bad.any(), (int(bad.sum()), np.argwhere(bad)[0].tolist(),
-                           float(np.abs(got - want)[bad].max()))
+    off = (got.double() - want).abs()
+    bad = ~(off <= tol)
+    assert not bool(bad.any()), (int(bad.sum()), bad.nonzero()[0].tolist(), float(off[bad].max()))
+
+
+def _d(a):
+    return None if a is None else a.double()
 
 
 def _inputs(n, d_in, d_out, dt, seed):
@@ -54,18 +56,18 @@ def _inputs(n, d_in, d_out, dt, seed):
 
 
 def _check_forward(x, w, b, r, act, preact, out_dt, result=None):
-    dev = x.device
-    np_ = lambda a: None if a is None else a.double().cpu().numpy()
-    X, W, B, R = np_(x), np_(w), np_(b), np_(r)
+    X, W, B, R = _d(x), _d(w), _d(b), _d(r)
     y, z = ops_plain.linear(X, W, B, R, act)
     res = result or lce.linear(x, w, b, r, activation=act, want_preact=preact, out_dtype=out_dt)
-    size = np.abs(X) @ np.abs(W).T + (0 if B is None else np.abs(B))
+    size = X.abs() @ W.abs().T + (0 if B is None else B.abs())
     e = (x.shape[1] + 1) * 2.0 ** -23 * size
     if preact:
         _within(res.preact, z, _round(z, e, x.dtype))
-    ey = 1.13 * e + (2.0 ** -20 * np.maximum(1.0, np.abs(z)) if act in ("gelu", "silu") else 0.0)
+    ey = 1.13 * e
+    if act in ("gelu", "silu"):
+        ey = ey + 2.0 ** -20 * z.abs().clamp(min=1.0)
     if R is not None:
-        ey = ey + 2.0 ** -23 * (np.abs(y) + np.abs(R))
+        ey = ey + 2.0 ** -23 * (y.abs() + R.abs())
     _within(res.out, y, _round(y, ey, out_dt))
     return res
 
@@ -89,24 +91,23 @@ def test_forward(n, d_in, d_out, dt):
 
 
 def _check_backward(dy, x, w, z, act, grads, x_values=None, z_values=None):
-    np_ = lambda a: a.double().cpu().numpy()
-    DY, W = np_(dy), np_(w)
-    X, Z = np_(x_values if x_values is not None else x), None
+    DY, W = _d(dy), _d(w)
+    X, Z = _d(x_values if x_values is not None else x), None
     if act != "none":
-        Z = np_(z_values if z_values is not None else z)
+        Z = _d(z_values if z_values is not None else z)
     dx, dw, db, g = ops_plain.linear_backward(DY, X, W, Z, act)
-    eg = np.zeros_like(g)
+    eg = torch.zeros_like(g)
     if act in ("gelu", "silu"):
-        eg = np.abs(DY) * 2.0 ** -20 * np.maximum(1.0, np.abs(Z)) + 2.0 ** -24 * np.abs(g)
+        eg = DY.abs() * 2.0 ** -20 * Z.abs().clamp(min=1.0) + 2.0 ** -24 * g.abs()
     er = eg if act == "none" else _round(g, eg, dy.dtype)
     n, m = g.shape
-    size = np.abs(g) + er
+    size = g.abs() + er
     if grads.d_x is not None:
-        _within(grads.d_x, dx, _round(dx, er @ np.abs(W) + m * 2.0 ** -23 * (size @ np.abs(W)),
+        _within(grads.d_x, dx, _round(dx, er @ W.abs() + m * 2.0 ** -23 * (size @ W.abs()),
                                       dy.dtype))
     if grads.d_weight is not None:
         _within(grads.d_weight, dw,
-                _round(dw, er.T @ np.abs(X) + n * 2.0 ** -23 * (size.T @ np.abs(X)),
+                _round(dw, er.T @ X.abs() + n * 2.0 ** -23 * (size.T @ X.abs()),
                        grads.d_weight.dtype))
     if grads.d_bias is not None:
         _within(grads.d_bias, db, _round(db, eg.sum(0) + n * 2.0 ** -23 * size.sum(0),
@@ -179,29 +180,26 @@ def test_gradients_against_differences(act):
     n, d_in, d_out = 37, 72, 50
     t = torch.bfloat16
     x, w, b, _, c = _inputs(n, d_in, d_out, t, 11)
-    X, W, B, C = (a.double().numpy() for a in (x, w, b, c))
+    X, W, B, C = (a.double() for a in (x, w, b, c))
     z = lce.linear(x.to(dev), w.to(dev), b.to(dev), activation=act, out_dtype=torch.float32,
                    want_preact=True).preact
     # the slope is taken at the stored (rounded) z: shift the bias to match it
-    shift = z.double().cpu().numpy() - (X @ W.T + B)
+    shift = z.double().cpu() - (X @ W.T + B)
     g = lce.linear_backward(c.to(dev), x.to(dev), w.to(dev), z, activation=act, want_bias=True)
     f = lambda X_, W_, B_: float((C * ops_plain.act(X_ @ W_.T + B_ + shift, act)).sum())
-    G = np.abs(C) * 1.2
-    rng = np.random.default_rng(12)
+    G = C.abs() * 1.2
+    gen = torch.Generator().manual_seed(12)
     h = 1e-4
     for _ in range(3):
-        for got, at, size in ((g.d_x, 0, G @ np.abs(W)), (g.d_weight, 1, G.T @ np.abs(X)),
+        for got, at, size in ((g.d_x, 0, G @ W.abs()), (g.d_weight, 1, G.T @ X.abs()),
                               (g.d_bias, 2, G.sum(0))):
             args = [X, W, B]
-            v = rng.standard_normal(args[at].shape)
+            v = torch.randn(args[at].shape, generator=gen, dtype=torch.float64)
             hi, lo = list(args), list(args)
             hi[at], lo[at] = args[at] + h * v, args[at] - h * v
             want = (f(*hi) - f(*lo)) / (2 * h)
-            tol = 2 * 2.0 ** -8 * float((size * np.abs(v)).sum()) + 1e-5
-            assert abs(float((got.double().cpu().numpy() * v).sum()) - want) <= tol
-            # and far closer than the bound in the usual case: signs cancel
-            assert abs(float((got.double().cpu().numpy() * v).sum()) - want) <= max(
-                1e-5, 0.02 * tol + 0.02 * abs(want))
+            tol = 2 * 2.0 ** -8 * float((size * v.abs()).sum()) + 1e-5
+            assert abs(float((got.double().cpu() * v).sum()) - want) <= tol
 
 
 def test_non_finite_values_stay_in_their_rows():
@@ -254,3 +252,87 @@ def test_same_bits_every_time():
             assert torch.equal(again.out, first.out) and torch.equal(again.preact, first.preact)
             for k in ("d_x", "d_weight", "d_bias"):
                 assert torch.equal(getattr(g1, k), getattr(g2, k)), k
+
+
+@pytest.mark.parametrize("n,d_in,d_out,act,dt", [
+    (20, 1024, 40000, "none", "bf16"),      # 128 x 32 tiles
+    (60, 1000, 40000, "silu", "fp16"),      # 128 x 64 tiles, an odd depth
+    (100, 8192, 72, "gelu", "bf16"),        # 64 x 64 tiles, the depth in 16 parts
+    (700, 512, 3000, "relu", "fp16"),       # 128 x 128 tiles
+    (777, 1003, 1531, "silu", "fp16"),      # padded copies of odd rows
+    (515, 1002, 777, "gelu", "bf16"),       # odd rows read as they lie
+    (4096, 512, 4096, "gelu", "bf16"),      # 256 x 256 tiles
+    (3000, 2601, 5300, "gelu", "fp16"),     # 256 x 256 tiles of padded copies
+    (130, 40, 20001, "none", "bf16")])
+def test_forward_on_every_core(n, d_in, d_out, act, dt):
+    dev = _dev()
+    t = TYPES[dt]
+    print(f"case linear {n}x{d_in}->{d_out} {dt} {act}", flush=True)
+    x, w, b, r, _ = (a.to(dev) for a in _inputs(n, d_in, d_out, t, 21))
+    _check_forward(x, w, b, r, act, True, t)
+    _check_forward(x, w, None, None, act, False, torch.float32)
+
+
+@pytest.mark.parametrize("n,d_in,d_out,act,dt", [
+    (5000, 72, 120, "silu", "bf16"),        # d_weight's depth in 16 parts
+    (515, 1003, 777, "silu", "fp16"),       # both products in one launch
+    (2100, 512, 1900, "gelu", "bf16"),
+    (8200, 1032, 4100, "gelu", "bf16"),     # 256 x 256 tiles, d_weight in 2 parts
+    (4100, 2056, 4224, "none", "fp16"),     # the same without copies of d_out_grad
+    (250, 65536, 1000, "relu", "bf16")])    # d_x from the weight as it lies
+def test_backward_on_every_core(n, d_in, d_out, act, dt):
+    dev = _dev()
+    t = TYPES[dt]
+    print(f"case linear backward {n}x{d_in}->{d_out} {dt} {act}", flush=True)
+    x, w, _, z, dy = (a.to(dev) for a in _inputs(n, d_in, d_out, t, 22))
+    g = lce.linear_backward(dy, x, w, z, activation=act, want_bias=True)
+    _check_backward(dy, x, w, z, act, g)
+    x8, z8 = lce.pack8(x), lce.pack8(z)
+    g = lce.linear_backward(dy, x8, w, z8, activation=act, weight_grad_dtype=t)
+    _check_backward(dy, x, w, z, act, g, lce.unpack8(x8), lce.unpack8(z8))
+    g = lce.linear_backward(dy, None, w, z, activation=act, want_weight=False)
+    _check_backward(dy, x, w, z, act, g)
+
+
+def test_more_than_32_bits_of_outputs():
+    """2^32 outputs and more: the last rows and columns are where they belong."""
+    dev = _dev()
+    n, d_in, d_out = 8200, 16, 1 << 19
+    x, w, b, _, _ = (a.to(dev) for a in _inputs(1, d_in, d_out, torch.bfloat16, 23))
+    x = torch.randn(n, d_in, generator=torch.Generator().manual_seed(24)).bfloat16().to(dev)
+    out = lce.linear(x, w, b, activation="relu").out
+    for rows in (slice(0, 2), slice(4095, 4098), slice(n - 2, n)):
+        _check_forward(x[rows], w, b, None, "relu", False, torch.bfloat16,
+                       lce.LinearResult(out[rows], None))
+
+
+def test_views_that_are_not_aligned_on_the_large_cores():
+    dev = _dev()
+    t = torch.bfloat16
+    off = lambda a, k: torch.cat([a.new_zeros(k), a.reshape(-1)])[k:].view(a.shape)
+    for n, d_in, d_out in ((4096, 512, 4096), (700, 512, 3000), (20, 1024, 40000)):
+        x, w, b, r, dy = (a.to(dev) for a in _inputs(n, d_in, d_out, t, 25))
+        _check_forward(off(x, 1), off(w, 3), b, off(r, 1), "gelu", True, t)
+        g = lce.linear_backward(off(dy, 1), off(x, 1), off(w, 1), off(r, 3), activation="gelu",
+                                want_bias=True)
+        _check_backward(dy, x, w, r, "gelu", g)
+
+
+@pytest.mark.parametrize("dt", ["bf16", "fp16"])
+def test_activations_at_the_ends(dt):
+    """Large, tiny and infinite pre-activations: what the formulas give in fp32."""
+    dev = _dev()
+    t = TYPES[dt]
+    v = torch.tensor([0.0, -0.0, 1e-4, -1e-4, 0.5, -0.5, 3.0, -3.0, 6.0, -6.0, 12.0, -12.0, 80.0,
+                      -80.0, 1e4, -1e4, 6e4, -6e4]).to(t)
+    x = v.view(-1, 1).to(dev)
+    w = torch.ones(1, 1, dtype=t, device=dev)
+    for act in ops_plain.ACTS:
+        _check_forward(x, w, None, None, act, True, t)
+        dy = torch.full_like(x, 0.5)
+        _check_backward(dy, x, w, x, act, lce.linear_backward(dy, x, w, x, activation=act))
+    inf = torch.tensor([[float("inf")], [-float("inf")], [float("nan")]], dtype=t, device=dev)
+    got = lce.linear(inf, w, activation="relu").out.view(-1)
+    assert got[0] == float("inf") and got[1] == 0 and bool(got[2].isnan())
+    got = lce.linear(inf, w, activation="gelu").out.view(-1)
+    assert got[0] == float("inf") and bool(got[2].isnan())
