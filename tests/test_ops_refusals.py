@@ -113,7 +113,7 @@ def test_beam_reorder_refusals():
 
 
 def test_linear_refusals():
-    n, d_in, d_out = 67, 10, 12
+    n, d_in, d_out = 70, 8200, 12           # (the depth in parts: a workspace)
     t = torch.bfloat16
     w = lce.lce_linear_workspace_bytes
     v = lce.lce_linear_backward_workspace_bytes
@@ -145,7 +145,7 @@ def test_linear_refusals():
     with pytest.raises(ValueError):
         lce.linear(base["x"], base["weight"])               # not on a GPU
     with pytest.raises(ValueError):
-        lce.linear(base["x"], base["weight"][:, :9])
+        lce.linear(base["x"], base["weight"][:, :9].contiguous())
 
     bw = dict(d_out_grad=torch.zeros(n, d_out, dtype=t), x=base["x"], x_scales=None,
               weight=base["weight"], preact=base["preact"], preact_scales=None, n_tok=n, d_in=d_in,
@@ -154,7 +154,7 @@ def test_linear_refusals():
               workspace=torch.zeros(v(n, d_in, d_out, t), dtype=U8), stream=0)
     call = lambda **kw: lce.lce_linear_backward(**{**bw, **kw})
     codes, zcodes = torch.zeros(n, d_in, dtype=U8), torch.zeros(n, d_out, dtype=U8)
-    scales, zscales = torch.zeros(n, 1, dtype=U8), torch.zeros(n, 1, dtype=U8)
+    scales, zscales = torch.zeros(n, 257, dtype=U8), torch.zeros(n, 1, dtype=U8)
     assert w(n, d_in, d_out, t) > 0 and w(3, d_in, d_out, t) == 0
     assert call(n_tok=0) == 581 and call(d_in=0) == 581 and call(d_out=0) == 581
     assert call(d_in=2 ** 16 + 1) == 583
