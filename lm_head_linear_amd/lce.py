@@ -8,7 +8,6 @@ first call raises: there is no fallback path.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 import functools
 import os
@@ -547,27 +546,27 @@ def ce_logits(logits, targets, loss_mask=None, z_coef=0.0, grad_out=1.0, want_gr
 
 # ------------------------------------------- operators next to the losses
 
-def _on(*tensors) -> torch.device:
-    """The one GPU that all given tensors are on; ValueError otherwise."""
-    dev = None
-    for x in tensors:
-        if x is None:
-            continue
-        if not x.is_cuda:
-            raise ValueError("tensors must be on a GPU")
-        if dev is None:
-            dev = x.device
-        elif x.device != dev:
-            raise ValueError("tensors must be on one device")
-    return dev
+_NONE = Tensor(None, 0, 0)
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 
 
-_HERE_ALREADY = contextlib.nullcontext()
+def _gpu(x: torch.Tensor) -> int:
+    """The index of the GPU that x is on; ValueError if it is on none."""
+    idx = x.get_device()
+    if idx < 0:
+        raise ValueError("tensors must be on a GPU")
+    return idx
 
 
-def _use(dev: torch.device):
-    """Context in which dev is the current device."""
-    return _HERE_ALREADY if torch.cuda.current_device() == dev.index else torch.cuda.device(dev)
+def _arg(x: Optional[torch.Tensor], idx: int) -> Tensor:
+    """_t(x) for a tensor that has to be on GPU idx."""
+    if x is None:
+        return _NONE
+    if x.get_device() != idx:
+        raise ValueError("tensors must be on one GPU")
+    if not x.is_contiguous():
+        raise ValueError("tensors must be contiguous")
+    return Tensor(x.data_ptr(), x.numel(), _DT.get(x.dtype, 0))
 
 
 @functools.lru_cache(maxsize=256)
@@ -614,19 +613,30 @@ class Packed8:
 def pack8(x) -> Packed8:
     """Allocate codes and scales, call lce_pack8."""
     n, d = x.shape
-    with _use(_on(x)):
-        codes = torch.empty(n, d, dtype=torch.uint8, device=x.device)
-        scales = torch.empty(n, -(-d // PACK8_BLOCK), dtype=torch.uint8, device=x.device)
-        _check(lce_pack8(x, n, d, codes, scales), "lce_pack8")
+    idx = _gpu(x)
+    if idx != _current_device():
+        with torch.cuda.device(idx):
+            return pack8(x)
+    dev = x.device
+    codes = torch.empty(n, d, dtype=torch.uint8, device=dev)
+    scales = torch.empty(n, -(-d // PACK8_BLOCK), dtype=torch.uint8, device=dev)
+    _check(lib().lce_pack8(_arg(x, idx), n, d, _arg(codes, idx), _arg(scales, idx), _stream(dev)),
+           "lce_pack8")
     return Packed8(codes, scales, x.dtype)
 
 
 def unpack8(packed: Packed8):
     """Allocate the 16-bit tensor, call lce_unpack8."""
-    n, d = packed.codes.shape
-    with _use(_on(packed.codes, packed.scales)):
-        out = torch.empty(n, d, dtype=packed.dtype, device=packed.codes.device)
-        _check(lce_unpack8(packed.codes, packed.scales, n, d, out), "lce_unpack8")
+    codes, scales = packed.codes, packed.scales
+    n, d = codes.shape
+    idx = _gpu(codes)
+    if idx != _current_device():
+        with torch.cuda.device(idx):
+            return unpack8(packed)
+    dev = codes.device
+    out = torch.empty(n, d, dtype=packed.dtype, device=dev)
+    _check(lib().lce_unpack8(_arg(codes, idx), _arg(scales, idx), n, d, _arg(out, idx),
+                             _stream(dev)), "lce_unpack8")
     return out
 
 
@@ -675,20 +685,24 @@ def beam_select(logits, scores, n_out, finished=None, allowed=None, eos=None, wo
     rows, V = logits.shape
     if rows != n_seq * beams:
         raise ValueError("logits need one row per beam")
-    dev = _on(logits, scores, finished, allowed, workspace)
-    with _use(dev):
-        ws = workspace
-        if ws is None:
-            ws = torch.empty(_bytes(lce_beam_workspace_bytes, n_seq, beams, V, n_out),
-                             dtype=torch.uint8, device=dev)
-        step = BeamStep(torch.empty(n_seq, n_out, dtype=torch.float32, device=dev),
-                        torch.empty(n_seq, n_out, dtype=torch.int64, device=dev),
-                        torch.empty(n_seq, n_out, dtype=torch.int64, device=dev),
-                        torch.empty(n_seq, n_out, dtype=torch.bool, device=dev))
-        _check(lce_beam_select(logits, scores, finished, allowed, n_seq, beams, V, n_out,
-                               -1 if eos is None else int(eos), step.scores, step.parents,
-                               step.tokens, step.finished, ws), "lce_beam_select")
-    return step
+    idx = _gpu(logits)
+    if idx != _current_device():
+        with torch.cuda.device(idx):
+            return beam_select(logits, scores, n_out, finished, allowed, eos, workspace)
+    dev = logits.device
+    if workspace is None:
+        workspace = torch.empty(_bytes(lce_beam_workspace_bytes, n_seq, beams, V, n_out),
+                                dtype=torch.uint8, device=dev)
+    best = torch.empty(n_seq, n_out, dtype=torch.float32, device=dev)
+    parents = torch.empty(n_seq, n_out, dtype=torch.int64, device=dev)
+    tokens = torch.empty(n_seq, n_out, dtype=torch.int64, device=dev)
+    done = torch.empty(n_seq, n_out, dtype=torch.bool, device=dev)
+    _check(lib().lce_beam_select(_arg(logits, idx), _arg(scores, idx), _arg(finished, idx),
+                                 _arg(allowed, idx), n_seq, beams, V, n_out,
+                                 -1 if eos is None else int(eos), _arg(best, idx),
+                                 _arg(parents, idx), _arg(tokens, idx), _arg(done, idx),
+                                 _arg(workspace, idx), _stream(dev)), "lce_beam_select")
+    return BeamStep(best, parents, tokens, done)
 
 
 def beam_reorder(states, parents, beams, out=None, length=None, dim=2):
@@ -697,6 +711,8 @@ def beam_reorder(states, parents, beams, out=None, length=None, dim=2):
     [n_seq*n_out][...]), or in place without it.  `length` carries over the
     first `length` entries of dimension `dim` only.  Returns the list written."""
     out = states if out is None else out
+    if len(out) != len(states):
+        raise ValueError("as many destinations as sources are needed")
     n_seq, n_out = parents.shape
     shape = states[0].shape[1:]
     for x, y in zip(states, out):
@@ -717,9 +733,15 @@ def beam_reorder(states, parents, beams, out=None, length=None, dim=2):
         for s in shape[dim:]:
             inner *= s
         elems, stride = length * inner, shape[dim - 1] * inner
-    with _use(_on(parents, *states, *out)):
-        _check(lce_beam_reorder(states, out, parents, n_seq, beams, n_out, segs, elems, stride),
-               "lce_beam_reorder")
+    idx = _gpu(parents)
+    if idx != _current_device():
+        with torch.cuda.device(idx):
+            return beam_reorder(states, parents, beams, out, length, dim)
+    n = len(states)
+    src = (Tensor * n)(*[_arg(x, idx) for x in states])
+    dst = src if out is states else (Tensor * n)(*[_arg(x, idx) for x in out])
+    _check(lib().lce_beam_reorder(src, dst, n, _arg(parents, idx), n_seq, beams, n_out, segs, elems,
+                                  stride, _stream(parents.device)), "lce_beam_reorder")
     return out
 
 
@@ -778,20 +800,24 @@ def linear(x, weight, bias=None, residual=None, activation="none", want_preact=F
     """act(x weight^T + bias) + residual: allocate out, preact (if wanted) and
     (if needed) the workspace, call lce_linear."""
     n, d_in = x.shape
-    d_out = weight.shape[0]
-    if weight.shape[1] != d_in or (bias is not None and bias.numel() != d_out) or (
+    d_out, k = weight.shape
+    if k != d_in or (bias is not None and bias.numel() != d_out) or (
             residual is not None and residual.shape != (n, d_out)):
         raise ValueError("weight, bias or residual does not fit x")
-    dev = _on(x, weight, bias, residual, workspace)
-    with _use(dev):
-        if workspace is None:
-            nbytes = _bytes(lce_linear_workspace_bytes, n, d_in, d_out, x.dtype)
-            if nbytes > 0:
-                workspace = torch.empty(nbytes, dtype=torch.uint8, device=dev)
-        out = torch.empty(n, d_out, dtype=out_dtype or x.dtype, device=dev)
-        preact = torch.empty(n, d_out, dtype=x.dtype, device=dev) if want_preact else None
-        _check(lce_linear(x, weight, bias, residual, n, d_in, d_out,
-                          ACTIVATIONS.get(activation, -1), preact, out, workspace), "lce_linear")
+    idx = _gpu(x)
+    if idx != _current_device():
+        with torch.cuda.device(idx):
+            return linear(x, weight, bias, residual, activation, want_preact, out_dtype, workspace)
+    dev, dtype = x.device, x.dtype
+    if workspace is None:
+        nbytes = _bytes(lce_linear_workspace_bytes, n, d_in, d_out, dtype)
+        if nbytes > 0:
+            workspace = torch.empty(nbytes, dtype=torch.uint8, device=dev)
+    out = torch.empty(n, d_out, dtype=out_dtype or dtype, device=dev)
+    preact = torch.empty(n, d_out, dtype=dtype, device=dev) if want_preact else None
+    _check(lib().lce_linear(_arg(x, idx), _arg(weight, idx), _arg(bias, idx), _arg(residual, idx), n,
+                            d_in, d_out, ACTIVATIONS.get(activation, -1), _arg(preact, idx),
+                            _arg(out, idx), _arg(workspace, idx), _stream(dev)), "lce_linear")
     return LinearResult(out, preact)
 
 
@@ -814,20 +840,30 @@ def linear_backward(d_out, x, weight, preact=None, activation="none", want_x=Tru
         raise ValueError("x or weight does not fit d_out")
     if accumulate and ((want_weight and d_weight is None) or (want_bias and d_bias is None)):
         raise ValueError("accumulate needs the gradients it adds to")
-    dev = _on(d_out, x, xs, weight, preact, zs, d_weight, d_bias, workspace)
-    with _use(dev):
-        if workspace is None:
-            workspace = torch.empty(
-                _bytes(lce_linear_backward_workspace_bytes, n, d_in, m, d_out.dtype),
-                dtype=torch.uint8, device=dev)
-        d_x = torch.empty(n, d_in, dtype=d_out.dtype, device=dev) if want_x else None
-        if want_weight and d_weight is None:
-            d_weight = torch.empty(m, d_in, dtype=weight_grad_dtype or torch.float32, device=dev)
-        if want_bias and d_bias is None:
-            d_bias = torch.empty(m, dtype=torch.float32, device=dev)
-        _check(lce_linear_backward(d_out, x, xs, weight, preact, zs, n, d_in, m,
-                                   ACTIVATIONS.get(activation, -1), d_x,
-                                   d_weight if want_weight else None,
-                                   d_bias if want_bias else None, accumulate, workspace),
-               "lce_linear_backward")
+    idx = _gpu(d_out)
+    if idx != _current_device():
+        with torch.cuda.device(idx):
+            return linear_backward(d_out, x if xs is None else Packed8(x, xs, d_out.dtype), weight,
+                                   preact if zs is None else Packed8(preact, zs, d_out.dtype),
+                                   activation, want_x, want_weight, want_bias, weight_grad_dtype,
+                                   d_weight, d_bias, accumulate, workspace)
+    dev = d_out.device
+    if workspace is None:
+        workspace = torch.empty(
+            _bytes(lce_linear_backward_workspace_bytes, n, d_in, m, d_out.dtype),
+            dtype=torch.uint8, device=dev)
+    d_x = torch.empty(n, d_in, dtype=d_out.dtype, device=dev) if want_x else None
+    if not want_weight:
+        d_weight = None
+    elif d_weight is None:
+        d_weight = torch.empty(m, d_in, dtype=weight_grad_dtype or torch.float32, device=dev)
+    if not want_bias:
+        d_bias = None
+    elif d_bias is None:
+        d_bias = torch.empty(m, dtype=torch.float32, device=dev)
+    _check(lib().lce_linear_backward(
+        _arg(d_out, idx), _arg(x, idx), _arg(xs, idx), _arg(weight, idx), _arg(preact, idx),
+        _arg(zs, idx), n, d_in, m, ACTIVATIONS.get(activation, -1), _arg(d_x, idx),
+        _arg(d_weight, idx), _arg(d_bias, idx), int(accumulate), _arg(workspace, idx),
+        _stream(dev)), "lce_linear_backward")
     return LinearGrads(d_x, d_weight, d_bias)
