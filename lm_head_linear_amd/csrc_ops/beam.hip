@@ -352,18 +352,6 @@ __device__ inline bool before(const BeamKey &a, const BeamKey &b) {
   return a.total > b.total || (a.total == b.total && a.place < b.place);
 }
 
-// (m, s) += (m2, s2) where s counts exp(x - m): the larger maximum carries on.
-__device__ inline void fold_sum(double &m, double &s, double m2, double s2) {
-  if (m2 > m) {
-    const double t = m;
-    m = m2; m2 = t;
-    const double u = s;
-    s = s2; s2 = u;
-  }
-  // (a maximum of -inf comes with a sum of 0, or of NaN, which stays)
-  s += s2 == 0.0 ? 0.0 : s2 * exp(m2 - m);
-}
-
 // One block per sequence.
 __global__ void __launch_bounds__(kBeamThreads) beam_merge_kernel(
     const uint64_t *cand, const PieceStats *stats, const float *scores, const uint8_t *finished,
@@ -379,21 +367,43 @@ __global__ void __launch_bounds__(kBeamThreads) beam_merge_kernel(
   __shared__ uint32_t s_group[kBeamGroups];
   __shared__ int s_count;
 
+  // the thread's first eight candidates, on their way while the rest begins
+  const int per_beam = pieces * n_out, total = beams * per_beam;
+  const uint64_t *keys = cand + seq * total;
+  uint64_t held[8];
+#pragma unroll
+  for (int u = 0; u < 8; ++u) {
+    const int i = tid + u * kBeamThreads;
+    held[u] = i < total ? keys[i] : 0;
+  }
   // normalisers: 32 lanes a beam, each folding the pieces it meets
-  const int per_beam = pieces * n_out;
   for (int k = tid >> 5; k < beams; k += kBeamThreads / 32) {
     const int64_t row = seq * beams + k;
     const float score = scores[row];
     const bool done = finished && finished[row];
-    double m = -INFINITY, sum = 0.0;
+    float top = -INFINITY;
+    double sum = 0.0;
     if (!done) {
-      for (int c = tid & 31; c < pieces; c += 32) {
-        const PieceStats st = stats[row * pieces + c];
-        fold_sum(m, sum, double(st.top), st.sum);
+      // the first 32 pieces are held, further ones (a vocabulary beyond 2^19)
+      // are read again
+      const int c0 = tid & 31;
+      PieceStats st = {0.0, -INFINITY, 0};
+      if (c0 < pieces) st = stats[row * pieces + c0];
+      top = st.top;
+      for (int c = c0 + 32; c < pieces; c += 32) top = fmaxf(top, stats[row * pieces + c].top);
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor(top, o));
+      const double m = top == -INFINITY ? 0.0 : double(top);
+      // (a maximum of -inf comes with a sum of 0, or of NaN, which stays)
+      sum = st.sum == 0.0 ? 0.0 : st.sum * exp(double(st.top) - m);
+      for (int c = c0 + 32; c < pieces; c += 32) {
+        st = stats[row * pieces + c];
+        if (st.sum != 0.0) sum += st.sum * exp(double(st.top) - m);
       }
 #pragma unroll
-      for (int o = 16; o > 0; o >>= 1) fold_sum(m, sum, __shfl_xor(m, o), __shfl_xor(sum, o));
+      for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor(sum, o);
     }
+    const double m = top == -INFINITY ? 0.0 : double(top);
     if ((tid & 31) == 0) {
       const double lse = m + log(sum);
       s_lse[k] = done ? 0.0 : lse;
@@ -407,15 +417,7 @@ __global__ void __launch_bounds__(kBeamThreads) beam_merge_kernel(
 
   // every candidate of the sequence that this thread looks at
   auto each = [&](auto &&use) {
-    const int total = beams * per_beam;
-    const uint64_t *p = cand + seq * total;
-    for (int i0 = tid; i0 < total; i0 += 8 * kBeamThreads) {
-      uint64_t key[8];                       // eight loads in flight
-#pragma unroll
-      for (int u = 0; u < 8; ++u) {
-        const int i = i0 + u * kBeamThreads;
-        key[u] = i < total ? p[i] : 0;
-      }
+    auto look = [&](const uint64_t (&key)[8], int i0) {
 #pragma unroll
       for (int u = 0; u < 8; ++u) {
         const uint32_t k = uint32_t(i0 + u * kBeamThreads) / uint32_t(per_beam);
@@ -423,6 +425,16 @@ __global__ void __launch_bounds__(kBeamThreads) beam_merge_kernel(
           use(BeamKey{order64(s_shift[k] + (double(unorder32(uint32_t(key[u] >> 32))) - s_lse[k])),
                       (k << 24) | ~uint32_t(key[u])});
       }
+    };
+    look(held, tid);
+    for (int i0 = tid + 8 * kBeamThreads; i0 < total; i0 += 8 * kBeamThreads) {
+      uint64_t key[8];                       // eight loads in flight
+#pragma unroll
+      for (int u = 0; u < 8; ++u) {
+        const int i = i0 + u * kBeamThreads;
+        key[u] = i < total ? keys[i] : 0;
+      }
+      look(key, i0);
     }
     if (tid < beams && s_state[tid] == 2)
       use(BeamKey{order64(s_shift[tid]), (uint32_t(tid) << 24) | uint32_t(eos)});
