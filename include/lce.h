@@ -426,8 +426,9 @@ int64_t lce_linear_backward_workspace_bytes(int64_t n_tok, int64_t d_in, int64_t
  *            where that is 0
  * Products are summed in fp32; bias, activation and residual are applied to
  * the fp32 sum, and out and preact are each rounded once.  The sums run in a
- * fixed order: the same call gives the same bits.  Only enqueues on
- * `stream`.  Statuses as the workspace query, 582 for a short buffer. */
+ * fixed order: the same call gives the same bits.  out (but for residual)
+ * and preact must not overlap another buffer.  Only enqueues on `stream`.
+ * Statuses as the workspace query, 582 for a short buffer. */
 int32_t lce_linear(const lce_tensor *x, const lce_tensor *weight, const lce_tensor *bias,
                    const lce_tensor *residual, int64_t n_tok, int64_t d_in, int64_t d_out,
                    int32_t activation, lce_tensor *preact, lce_tensor *out, lce_tensor *workspace,
@@ -486,7 +487,7 @@ int32_t lce_unpack8(const lce_tensor *codes, const lce_tensor *scales, int64_t n
 /* Bytes of device workspace lce_beam_select needs (-status if refused: 581
  * for a dimension < 1; 583 for beams > 32, n_out > 64, n_seq > LCE_MAX_N_TOK
  * or vocab > LCE_MAX_VOCAB; 584 when the rows have 2^24 or more pieces of
- * 8192 values). */
+ * 16384 values, each row at least one). */
 int64_t lce_beam_workspace_bytes(int64_t n_seq, int64_t beams, int64_t vocab, int64_t n_out);
 
 /* The n_out best continuations of every sequence: with
@@ -529,9 +530,11 @@ int32_t lce_beam_select(const lce_tensor *logits, const lce_tensor *scores,
  *             src[i].numel >= n_seq*beams*segs*seg_stride and
  *             dst[i].numel >= n_seq*n_out*segs*seg_stride.  Either every dst
  *             is its src (in place; needs n_out == beams, and rows that stay
- *             are not touched) or none overlaps it (582 otherwise)
+ *             are not touched) or none overlaps any src; no two destinations
+ *             overlap, and none overlaps parents (582 otherwise)
  *   parents   [n_seq*n_out] LCE_I64
- *   beams, n_out  at most 32 (583); the elements of a state at most 2^46 (584)
+ *   beams, n_out  at most 32, n_states at most 1024 (583); the elements of a
+ *             state at most 2^46 (584)
  * Only enqueues on `stream`. */
 int32_t lce_beam_reorder(const lce_tensor *src, lce_tensor *dst, int32_t n_states,
                          const lce_tensor *parents, int64_t n_seq, int64_t beams, int64_t n_out,

@@ -23,6 +23,8 @@
 // ranks the candidates of all beams by the same kind of threshold.
 #include <math.h>
 
+#include <algorithm>
+
 #include "ops_common.h"
 
 namespace lce {
@@ -512,6 +514,10 @@ __global__ void __launch_bounds__(kBeamThreads) beam_merge_kernel(
 // ------------------------------------------------------------- reordering --
 
 constexpr int kMaxStates = 64;     // states per launch
+constexpr int kMostStates = 1024;  // states per call
+struct Span {
+  uintptr_t begin, end;
+};
 struct StateList {
   const char *src[kMaxStates];
   char *dst[kMaxStates];
@@ -672,7 +678,8 @@ int32_t lce_beam_reorder(const lce_tensor *src, lce_tensor *dst, int32_t n_state
   if (n_states < 1 || n_seq < 1 || beams < 1 || n_out < 1 || segs < 1 || seg_elems < 0 ||
       seg_stride < 1)
     return LCE_EMPTY_DIMENSION;
-  if (n_seq > LCE_MAX_N_TOK || beams > kMaxBeams || n_out > kMaxBeams) return LCE_DIMENSION_TOO_LARGE;
+  if (n_seq > LCE_MAX_N_TOK || beams > kMaxBeams || n_out > kMaxBeams || n_states > kMostStates)
+    return LCE_DIMENSION_TOO_LARGE;
   // the elements of one state: within 2^46
   const int64_t most = beams > n_out ? beams : n_out;
   if (!lce_work_fits(segs, seg_stride, n_seq * most, LCE_MAX_WORK_CELLS))
@@ -686,16 +693,33 @@ int32_t lce_beam_reorder(const lce_tensor *src, lce_tensor *dst, int32_t n_state
       return LCE_DTYPE_MISMATCH;
   if (seg_elems > seg_stride || !holds(parents, n_seq * n_out)) return LCE_LENGTH_MISMATCH;
   const int64_t row = segs * seg_stride;
+  // every destination by itself, and no source in one but its own
+  Span to[kMostStates];
+  const uintptr_t from_bytes = uintptr_t(n_seq * beams * row) * size;
+  const uintptr_t to_bytes = uintptr_t(n_seq * n_out * row) * size;
   for (int32_t i = 0; i < n_states; ++i) {
     if (!holds(&src[i], n_seq * beams * row) || !holds(&dst[i], n_seq * n_out * row))
       return LCE_LENGTH_MISMATCH;
-    const char *a = static_cast<const char *>(src[i].data);
-    const char *b = static_cast<const char *>(dst[i].data);
-    if (i == 0) same = a == b;
-    if (same != (a == b) || (same && n_out != beams)) return LCE_LENGTH_MISMATCH;
-    const int64_t an = n_seq * beams * row * int64_t(size), bn = n_seq * n_out * row * int64_t(size);
-    if (!same && a < b + bn && b < a + an) return LCE_LENGTH_MISMATCH;   // they overlap
+    const bool here = src[i].data == dst[i].data;
+    if (i == 0) same = here;
+    if (same != here || (same && n_out != beams)) return LCE_LENGTH_MISMATCH;
+    const uintptr_t at = reinterpret_cast<uintptr_t>(dst[i].data);
+    to[i] = {at, at + to_bytes};
   }
+  std::sort(to, to + n_states, [](const Span &a, const Span &b) { return a.begin < b.begin; });
+  for (int32_t i = 1; i < n_states; ++i)
+    if (to[i].begin < to[i - 1].end) return LCE_LENGTH_MISMATCH;
+  auto meets = [&](uintptr_t begin, uintptr_t end) {
+    const Span *s = std::upper_bound(to, to + n_states, begin,
+                                     [](uintptr_t x, const Span &t) { return x < t.end; });
+    return s != to + n_states && s->begin < end;
+  };
+  for (int32_t i = 0; !same && i < n_states; ++i) {
+    const uintptr_t at = reinterpret_cast<uintptr_t>(src[i].data);
+    if (meets(at, at + from_bytes)) return LCE_LENGTH_MISMATCH;
+  }
+  const uintptr_t order = reinterpret_cast<uintptr_t>(parents->data);
+  if (meets(order, order + uintptr_t(n_seq * n_out) * 8)) return LCE_LENGTH_MISMATCH;
   if (seg_elems == 0) return LCE_OK;
 
   (void)hipGetLastError();

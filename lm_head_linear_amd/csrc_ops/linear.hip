@@ -658,7 +658,11 @@ static int32_t plan_linear_backward(int64_t n, int64_t d_in, int64_t d_out, int3
   p->ld_out = round_to(d_out, 64);
   p->ld_n = round_to(n, 64);
   if (!offsets_fit(p->ld_out)) p->px = p->pw = ProductPlan{};
-  else if (!offsets_fit(p->ld_n) && p->pw.core != k256x256) p->pw = ProductPlan{};
+  else if (!offsets_fit(p->ld_n) && p->pw.core != k256x256) {
+    // (more than 4 million tokens: transposed copies would be too wide)
+    p->pw = ProductPlan{k256x256, 16, round_to(ceil_div(n, 16), 64)};
+    p->pw.part_bytes = size_t(16 * d_out * round_to(d_in, 8)) * 4;
+  }
   // Only the 256 x 256 core takes operands that are not K-major.  d_weight's
   // two are so as they lie and cost it nothing (8192 x 4096 x 4096: 231 us
   // against 225 K-major); d_x's W beside K-major G costs a fifth (286 us), more

@@ -294,6 +294,16 @@ def test_backward_on_every_core(n, d_in, d_out, act, dt):
     _check_backward(dy, x, w, z, act, g)
 
 
+@pytest.mark.parametrize("n,d_in,d_out", [(3, 16, (1 << 22) + 100), ((1 << 22) + 100, 8, 24)])
+def test_backward_of_very_long_dimensions(n, d_in, d_out):
+    """Rows and depths whose 256-fold byte offsets pass 31 bits."""
+    dev = _dev()
+    t = torch.bfloat16
+    x, w, _, z, dy = (a.to(dev) for a in _inputs(n, d_in, d_out, t, 26))
+    g = lce.linear_backward(dy, x, w, z, activation="relu", want_bias=True)
+    _check_backward(dy, x, w, z, "relu", g)
+
+
 def test_more_than_32_bits_of_outputs():
     """2^32 outputs and more: the last rows and columns are where they belong."""
     dev = _dev()

@@ -105,6 +105,16 @@ def test_beam_reorder_refusals():
     assert call(src=[room[:6]], dst=[room[1:]]) == 582
     assert call(src=[src[0], room[:6]], dst=[src[0], torch.zeros(6, 20)]) == 582
     assert call(src=[room[:6]], dst=[room[:6]], n_out=2, parents=p) == 582
+    # one state twice, states that change places, a destination in the parents
+    assert call(src=[src[0]] * 2, dst=[src[0]] * 2) == 582
+    assert call(src=src * 2, dst=dst * 2) == 582
+    a, b, c = (torch.zeros(6, 20) for _ in range(3))
+    assert call(src=[a, b], dst=[b, a]) == 582
+    assert call(src=[a, b], dst=[c, a]) == 582
+    words = torch.zeros(6, 20, dtype=torch.int64)
+    assert call(src=[torch.zeros_like(words)], dst=[words], parents=words.view(-1)[30:36]) == 582
+    assert call(src=[torch.zeros(6, 20) for _ in range(1025)],
+                dst=[torch.zeros(6, 20) for _ in range(1025)]) == 583
     assert call(seg_elems=0) == 580                     # nothing to carry over
     with pytest.raises(ValueError):
         lce.beam_reorder(src, p, beams)
