@@ -15,6 +15,7 @@ from concurrent.futures import ThreadPoolExecutor
 HERE = os.path.dirname(os.path.abspath(__file__))
 INCLUDE = os.path.join(os.path.dirname(HERE), "include")
 LIB = os.path.join(HERE, "liblce.so")
+BINDING = os.path.join(HERE, "_lce_torch.so")     # torch tensors -> liblce.so
 OBJ_DIR = os.path.join(HERE, "_build")
 
 # csrc/ holds the losses, csrc_ops/ the operators that stand next to them.
@@ -43,10 +44,46 @@ def _compile(src: str) -> str:
     return obj
 
 
+def _compile_binding() -> str:
+    """Compile the torch binding (host code only)."""
+    import sysconfig
+
+    from torch.utils import cpp_extension
+
+    obj = os.path.join(OBJ_DIR, "torch_binding.cpp.o")
+    rocm = os.environ.get("ROCM_PATH", "/opt/rocm")
+    includes = [INCLUDE, *cpp_extension.include_paths(), os.path.join(rocm, "include"),
+                sysconfig.get_paths()["include"]]
+    cmd = ["g++", "-O2", "-fPIC", "-std=c++17", "-D__HIP_PLATFORM_AMD__=1", "-DUSE_ROCM=1",
+           "-DTORCH_EXTENSION_NAME=_lce_torch", *[f"-I{i}" for i in includes], "-c",
+           os.path.join(HERE, "csrc_ops", "torch_binding.cpp"), "-o", obj]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        sys.stderr.write(r.stdout + r.stderr)
+        raise RuntimeError("compile failed: torch_binding.cpp")
+    return obj
+
+
+def _link_binding(obj: str) -> None:
+    from torch.utils import cpp_extension
+
+    tmp = BINDING + ".tmp"
+    cmd = ["g++", "-shared", "-fPIC", "-Wl,-rpath,$ORIGIN", "-o", tmp, obj, f"-L{HERE}", "-l:liblce.so",
+           *[f"-L{d}" for d in cpp_extension.library_paths()], "-lc10", "-lc10_hip", "-ltorch_cpu",
+           "-ltorch", "-ltorch_python"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        sys.stderr.write(r.stdout + r.stderr)
+        raise RuntimeError("link failed: _lce_torch.so")
+    os.replace(tmp, BINDING)
+
+
 def build(verbose: bool = False) -> str:
     os.makedirs(OBJ_DIR, exist_ok=True)
-    with ThreadPoolExecutor(max_workers=len(SOURCES)) as ex:
+    with ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
+        binding = ex.submit(_compile_binding)
         objs = list(ex.map(_compile, SOURCES))
+        binding_obj = binding.result()
     tmp = LIB + ".tmp"
     # -z defs: an unresolved symbol (e.g. a kernel stub the host pass dropped)
     # fails the link instead of the first dlopen.
@@ -56,6 +93,7 @@ def build(verbose: bool = False) -> str:
         sys.stderr.write(r.stdout + r.stderr)
         raise RuntimeError("link failed")
     os.replace(tmp, LIB)
+    _link_binding(binding_obj)
     if verbose:
         print(f"built {LIB}")
     return LIB

@@ -1,7 +1,8 @@
 """Thin Python binding of liblce.so (include/lce.h).
 
-Argument marshalling only: every step of the computation runs in the HIP
-kernels of liblce.so.  Functions carry the C names; tensors are torch
+Argument marshalling only (by ctypes; the allocating calls of the operators
+next to the losses, which are short, go through the compiled _lce_torch.so):
+every step of the computation runs in the HIP kernels of liblce.so.  Functions carry the C names; tensors are torch
 tensors (device tensors for the device entry points), the stream is torch's
 current stream on the tensors' device.  If the library has not been built the
 first call raises: there is no fallback path.
@@ -9,7 +10,6 @@ first call raises: there is no fallback path.
 from __future__ import annotations
 
 import ctypes
-import functools
 import os
 from dataclasses import dataclass
 from typing import Optional
@@ -546,36 +546,22 @@ def ce_logits(logits, targets, loss_mask=None, z_coef=0.0, grad_out=1.0, want_gr
 
 # ------------------------------------------- operators next to the losses
 
-_NONE = Tensor(None, 0, 0)
-_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+_native = None
 
 
-def _gpu(x: torch.Tensor) -> int:
-    """The index of the GPU that x is on; ValueError if it is on none."""
-    idx = x.get_device()
-    if idx < 0:
-        raise ValueError("tensors must be on a GPU")
-    return idx
-
-
-def _arg(x: Optional[torch.Tensor], idx: int) -> Tensor:
-    """_t(x) for a tensor that has to be on GPU idx."""
-    if x is None:
-        return _NONE
-    if x.get_device() != idx:
-        raise ValueError("tensors must be on one GPU")
-    if not x.is_contiguous():
-        raise ValueError("tensors must be contiguous")
-    return Tensor(x.data_ptr(), x.numel(), _DT.get(x.dtype, 0))
-
-
-@functools.lru_cache(maxsize=256)
-def _bytes(query, *shape) -> int:
-    """A workspace query's answer (which depends on its arguments alone)."""
-    n = query(*shape)
-    if n < 0:
-        raise LceError(-n, query.__name__)
-    return n
+def _torch_calls():
+    """The compiled half of the allocating conveniences below (_lce_torch.so,
+    which calls liblce.so); raises if it is missing."""
+    global _native
+    if _native is None:
+        lib()
+        try:
+            from . import _lce_torch
+        except ImportError as e:
+            raise RuntimeError(f"_lce_torch.so is not built ({e}); run "
+                               "__graft_entry__.build() first") from e
+        _native = _lce_torch
+    return _native
 
 
 def _check(st: int, where: str):
@@ -612,31 +598,15 @@ class Packed8:
 
 def pack8(x) -> Packed8:
     """Allocate codes and scales, call lce_pack8."""
-    n, d = x.shape
-    idx = _gpu(x)
-    if idx != _current_device():
-        with torch.cuda.device(idx):
-            return pack8(x)
-    dev = x.device
-    codes = torch.empty(n, d, dtype=torch.uint8, device=dev)
-    scales = torch.empty(n, -(-d // PACK8_BLOCK), dtype=torch.uint8, device=dev)
-    _check(lib().lce_pack8(_arg(x, idx), n, d, _arg(codes, idx), _arg(scales, idx), _stream(dev)),
-           "lce_pack8")
+    st, codes, scales = _torch_calls().pack8(x)
+    _check(st, "lce_pack8")
     return Packed8(codes, scales, x.dtype)
 
 
 def unpack8(packed: Packed8):
     """Allocate the 16-bit tensor, call lce_unpack8."""
-    codes, scales = packed.codes, packed.scales
-    n, d = codes.shape
-    idx = _gpu(codes)
-    if idx != _current_device():
-        with torch.cuda.device(idx):
-            return unpack8(packed)
-    dev = codes.device
-    out = torch.empty(n, d, dtype=packed.dtype, device=dev)
-    _check(lib().lce_unpack8(_arg(codes, idx), _arg(scales, idx), n, d, _arg(out, idx),
-                             _stream(dev)), "lce_unpack8")
+    st, out = _torch_calls().unpack8(packed.codes, packed.scales, packed.dtype)
+    _check(st, "lce_unpack8")
     return out
 
 
@@ -678,30 +648,13 @@ class BeamStep:
     finished: torch.Tensor
 
 
-def beam_select(logits, scores, n_out, finished=None, allowed=None, eos=None, workspace=None):
+def beam_select(logits, scores, n_out, finished=None, allowed=None, eos=None,
+                workspace=None) -> BeamStep:
     """Allocate the outputs and (if needed) the workspace, call lce_beam_select
     for logits [n_seq*beams][vocab] and scores [n_seq][beams]."""
-    n_seq, beams = scores.shape
-    rows, V = logits.shape
-    if rows != n_seq * beams:
-        raise ValueError("logits need one row per beam")
-    idx = _gpu(logits)
-    if idx != _current_device():
-        with torch.cuda.device(idx):
-            return beam_select(logits, scores, n_out, finished, allowed, eos, workspace)
-    dev = logits.device
-    if workspace is None:
-        workspace = torch.empty(_bytes(lce_beam_workspace_bytes, n_seq, beams, V, n_out),
-                                dtype=torch.uint8, device=dev)
-    best = torch.empty(n_seq, n_out, dtype=torch.float32, device=dev)
-    parents = torch.empty(n_seq, n_out, dtype=torch.int64, device=dev)
-    tokens = torch.empty(n_seq, n_out, dtype=torch.int64, device=dev)
-    done = torch.empty(n_seq, n_out, dtype=torch.bool, device=dev)
-    _check(lib().lce_beam_select(_arg(logits, idx), _arg(scores, idx), _arg(finished, idx),
-                                 _arg(allowed, idx), n_seq, beams, V, n_out,
-                                 -1 if eos is None else int(eos), _arg(best, idx),
-                                 _arg(parents, idx), _arg(tokens, idx), _arg(done, idx),
-                                 _arg(workspace, idx), _stream(dev)), "lce_beam_select")
+    st, best, parents, tokens, done = _torch_calls().beam_select(
+        logits, scores, n_out, finished, allowed, -1 if eos is None else eos, workspace)
+    _check(st, "lce_beam_select")
     return BeamStep(best, parents, tokens, done)
 
 
@@ -711,37 +664,8 @@ def beam_reorder(states, parents, beams, out=None, length=None, dim=2):
     [n_seq*n_out][...]), or in place without it.  `length` carries over the
     first `length` entries of dimension `dim` only.  Returns the list written."""
     out = states if out is None else out
-    if len(out) != len(states):
-        raise ValueError("as many destinations as sources are needed")
-    n_seq, n_out = parents.shape
-    shape = states[0].shape[1:]
-    for x, y in zip(states, out):
-        if (x.shape[0] != n_seq * beams or y.shape[0] != n_seq * n_out or x.shape[1:] != shape
-                or y.shape[1:] != shape):
-            raise ValueError("states need one shape and one row per beam")
-    size = 1
-    for s in shape:
-        size *= s
-    if length is None:
-        segs, elems, stride = 1, size, size
-    else:
-        if not (1 <= dim <= len(shape) and 0 <= length <= shape[dim - 1]):
-            raise ValueError("length is outside the dimension")
-        segs, inner = 1, 1
-        for s in shape[:dim - 1]:
-            segs *= s
-        for s in shape[dim:]:
-            inner *= s
-        elems, stride = length * inner, shape[dim - 1] * inner
-    idx = _gpu(parents)
-    if idx != _current_device():
-        with torch.cuda.device(idx):
-            return beam_reorder(states, parents, beams, out, length, dim)
-    n = len(states)
-    src = (Tensor * n)(*[_arg(x, idx) for x in states])
-    dst = src if out is states else (Tensor * n)(*[_arg(x, idx) for x in out])
-    _check(lib().lce_beam_reorder(src, dst, n, _arg(parents, idx), n_seq, beams, n_out, segs, elems,
-                                  stride, _stream(parents.device)), "lce_beam_reorder")
+    _check(_torch_calls().beam_reorder(states, parents, beams, out, length, dim),
+           "lce_beam_reorder")
     return out
 
 
@@ -799,25 +723,10 @@ def linear(x, weight, bias=None, residual=None, activation="none", want_preact=F
            out_dtype=None, workspace=None) -> LinearResult:
     """act(x weight^T + bias) + residual: allocate out, preact (if wanted) and
     (if needed) the workspace, call lce_linear."""
-    n, d_in = x.shape
-    d_out, k = weight.shape
-    if k != d_in or (bias is not None and bias.numel() != d_out) or (
-            residual is not None and residual.shape != (n, d_out)):
-        raise ValueError("weight, bias or residual does not fit x")
-    idx = _gpu(x)
-    if idx != _current_device():
-        with torch.cuda.device(idx):
-            return linear(x, weight, bias, residual, activation, want_preact, out_dtype, workspace)
-    dev, dtype = x.device, x.dtype
-    if workspace is None:
-        nbytes = _bytes(lce_linear_workspace_bytes, n, d_in, d_out, dtype)
-        if nbytes > 0:
-            workspace = torch.empty(nbytes, dtype=torch.uint8, device=dev)
-    out = torch.empty(n, d_out, dtype=out_dtype or dtype, device=dev)
-    preact = torch.empty(n, d_out, dtype=dtype, device=dev) if want_preact else None
-    _check(lib().lce_linear(_arg(x, idx), _arg(weight, idx), _arg(bias, idx), _arg(residual, idx), n,
-                            d_in, d_out, ACTIVATIONS.get(activation, -1), _arg(preact, idx),
-                            _arg(out, idx), _arg(workspace, idx), _stream(dev)), "lce_linear")
+    st, out, preact = _torch_calls().linear(x, weight, bias, residual,
+                                            ACTIVATIONS.get(activation, -1), want_preact, out_dtype,
+                                            workspace)
+    _check(st, "lce_linear")
     return LinearResult(out, preact)
 
 
@@ -829,41 +738,13 @@ def linear_backward(d_out, x, weight, preact=None, activation="none", want_x=Tru
     workspace, call lce_linear_backward.  x and preact may each be a Packed8;
     x may be None without want_weight, weight without want_x.  d_weight and
     d_bias may be given, and are added to with accumulate."""
-    n, m = d_out.shape
     xs = zs = None
     if isinstance(x, Packed8):
         x, xs = x.codes, x.scales
     if isinstance(preact, Packed8):
         preact, zs = preact.codes, preact.scales
-    d_in = weight.shape[1] if weight is not None else x.shape[1]
-    if (x is not None and x.shape != (n, d_in)) or (weight is not None and weight.shape[0] != m):
-        raise ValueError("x or weight does not fit d_out")
-    if accumulate and ((want_weight and d_weight is None) or (want_bias and d_bias is None)):
-        raise ValueError("accumulate needs the gradients it adds to")
-    idx = _gpu(d_out)
-    if idx != _current_device():
-        with torch.cuda.device(idx):
-            return linear_backward(d_out, x if xs is None else Packed8(x, xs, d_out.dtype), weight,
-                                   preact if zs is None else Packed8(preact, zs, d_out.dtype),
-                                   activation, want_x, want_weight, want_bias, weight_grad_dtype,
-                                   d_weight, d_bias, accumulate, workspace)
-    dev = d_out.device
-    if workspace is None:
-        workspace = torch.empty(
-            _bytes(lce_linear_backward_workspace_bytes, n, d_in, m, d_out.dtype),
-            dtype=torch.uint8, device=dev)
-    d_x = torch.empty(n, d_in, dtype=d_out.dtype, device=dev) if want_x else None
-    if not want_weight:
-        d_weight = None
-    elif d_weight is None:
-        d_weight = torch.empty(m, d_in, dtype=weight_grad_dtype or torch.float32, device=dev)
-    if not want_bias:
-        d_bias = None
-    elif d_bias is None:
-        d_bias = torch.empty(m, dtype=torch.float32, device=dev)
-    _check(lib().lce_linear_backward(
-        _arg(d_out, idx), _arg(x, idx), _arg(xs, idx), _arg(weight, idx), _arg(preact, idx),
-        _arg(zs, idx), n, d_in, m, ACTIVATIONS.get(activation, -1), _arg(d_x, idx),
-        _arg(d_weight, idx), _arg(d_bias, idx), int(accumulate), _arg(workspace, idx),
-        _stream(dev)), "lce_linear_backward")
+    st, d_x, d_weight, d_bias = _torch_calls().linear_backward(
+        d_out, x, xs, weight, preact, zs, ACTIVATIONS.get(activation, -1), want_x, want_weight,
+        want_bias, weight_grad_dtype or torch.float32, d_weight, d_bias, accumulate, workspace)
+    _check(st, "lce_linear_backward")
     return LinearGrads(d_x, d_weight, d_bias)
