@@ -363,29 +363,41 @@ __global__ void __launch_bounds__(T::NT) backward_kernel(TileParams g0, OutEpi<T
   bias_grad_block<T::F16>(bias, b - g1.blocks, reinterpret_cast<float *>(smem));
 }
 
-// Adds a product's K-splits ([split][cols][ld] fp32) in order and finishes.
+// Adds the K-splits ([split][cols][ld] fp32) of one or two products in order
+// and finishes.
+struct FoldJob {
+  const float *part;
+  int64_t ld, stride;
+  int32_t splits;
+  uint32_t blocks;       // 0: nothing to fold
+  OutParams out;
+};
 template <bool F16>
-__global__ void __launch_bounds__(256) fold_kernel(const float *part, int64_t ld, int64_t stride,
-                                                   int splits, OutParams out) {
-  const int64_t per_row = ld / 8, total = per_row * out.cols;
-  for (int64_t u = int64_t(blockIdx.x) * 256 + threadIdx.x; u < total;
-       u += int64_t(gridDim.x) * 256) {
+__device__ __forceinline__ void fold_block(const FoldJob &j, uint32_t bid) {
+  const int64_t per_row = j.ld / 8, total = per_row * j.out.cols;
+  for (int64_t u = int64_t(bid) * 256 + threadIdx.x; u < total; u += int64_t(j.blocks) * 256) {
     const int64_t c = u / per_row, m = (u - c * per_row) * 8;
-    const int count = out.rows - m >= 8 ? 8 : int(out.rows - m);
+    const int count = j.out.rows - m >= 8 ? 8 : int(j.out.rows - m);
     float z[8] = {0, 0, 0, 0, 0, 0, 0, 0}, b[8];
-    const float *p = part + c * ld + m;
-    for (int s = 0; s < splits; ++s, p += stride) {
-      const u32x4 x = *reinterpret_cast<const u32x4 *>(p);
-      const u32x4 y = *reinterpret_cast<const u32x4 *>(p + 4);
+    const float *p = j.part + c * j.ld + m;
+#pragma unroll 4
+    for (int s = 0; s < j.splits; ++s) {
+      const u32x4 x = *reinterpret_cast<const u32x4 *>(p + s * j.stride);
+      const u32x4 y = *reinterpret_cast<const u32x4 *>(p + s * j.stride + 4);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         z[i] += __uint_as_float(x[i]);
         z[4 + i] += __uint_as_float(y[i]);
       }
     }
-    load_bias<F16, 8>(out, m, count, b);
-    finish<F16, 8>(out, z, b, m, c, count, 0);
+    load_bias<F16, 8>(j.out, m, count, b);
+    finish<F16, 8>(j.out, z, b, m, c, count, 0);
   }
+}
+template <bool F16>
+__global__ void __launch_bounds__(256) fold_kernel(FoldJob a, FoldJob b) {
+  if (blockIdx.x < a.blocks) fold_block<F16>(a, blockIdx.x);
+  else fold_block<F16>(b, blockIdx.x - a.blocks);
 }
 
 // ------------------------------------------------------------------- host --
@@ -402,7 +414,12 @@ struct ProductPlan {
   Core core = kGeneric;
   int64_t splits = 1, k_per_split = 0;
   size_t part_bytes = 0;    // fp32 partial results of the splits
+  double us = 0.0;          // modelled
 };
+
+static size_t partial_bytes(int64_t M, int64_t N, int64_t splits) {
+  return splits > 1 ? size_t(splits * N * round_to(M, 8)) * 4 : 0;
+}
 
 struct Operand {
   const void *p;
@@ -432,7 +449,15 @@ static const TileCost kTiles[] = {
 };
 constexpr double kBytesPerUs = 5.0e6;    // what a large copy moves
 
-static ProductPlan plan_product(int64_t M, int64_t N, int64_t K) {
+constexpr int64_t kMostSplits = 32;
+
+// Microseconds that a product's K-splits add: a launch, and the partial
+// results written and read.
+static double fold_us(int64_t M, int64_t N, int64_t splits) {
+  return splits > 1 ? 3.0 + double(splits) * double(M) * double(N) * 8.0 / kBytesPerUs : 0.0;
+}
+
+static ProductPlan plan_product(int64_t M, int64_t N, int64_t K, bool few) {
   ProductPlan best;
   double best_us = 1e30;
   const int64_t steps = ceil_div(K, 64);
@@ -440,7 +465,7 @@ static ProductPlan plan_product(int64_t M, int64_t N, int64_t K) {
   for (const TileCost &t : kTiles) {
     if (t.core == k128x32 && N > 32) continue;
     const int64_t tiles = tile_count(M, N, t.bm, t.bn);
-    for (int64_t sp = 1; sp <= 16 && sp <= steps; sp *= 2) {
+    for (int64_t sp = 1; sp <= kMostSplits && sp <= steps; sp *= 2) {
       const int64_t per = ceil_div(steps, sp);
       if ((sp - 1) * per >= steps) continue;
       const int64_t all = tiles * sp, last = all % t.at_once;
@@ -448,8 +473,7 @@ static ProductPlan plan_product(int64_t M, int64_t N, int64_t K) {
       if (last)
         us += t.round + double(per) * (last <= kComputeUnits ? t.step_alone : t.step_shared);
       if (us < memory_us) us = memory_us;
-      // the fold: a launch, and the partial results written and read
-      if (sp > 1) us += 3.0 + double(sp) * double(M) * double(N) * 8.0 / kBytesPerUs;
+      us += fold_us(M, N, sp);
       if (us < best_us) {
         best_us = us;
         best.core = t.core;
@@ -458,11 +482,12 @@ static ProductPlan plan_product(int64_t M, int64_t N, int64_t K) {
       }
     }
   }
-  best.part_bytes = best.splits > 1 ? size_t(best.splits * N * round_to(M, 8)) * 4 : 0;
+  best.part_bytes = partial_bytes(M, N, best.splits);
+  best.us = best_us;
   // up to 64 rows may stream A instead: bound by the read of A, at a rate that
   // falls with the rows that share a wave (4.8, 2.9 and 1.9 TB/s measured for
   // up to 16, 32 and 64 rows of 32768 x 4096), with no ring to fill first
-  if (N <= kFewTokens) {
+  if (few && N <= kFewTokens) {
     const double floor_us = N <= 16 ? 4.8 : N <= 32 ? 5.7 : 7.5;
     const double rate = N <= 16 ? 4.8e6 : N <= 32 ? 2.9e6 : 1.9e6;
     const double us = 2.0 + 2.0 * double(M) * double(K) / rate;
@@ -472,6 +497,38 @@ static ProductPlan plan_product(int64_t M, int64_t N, int64_t K) {
     }
   }
   return best;
+}
+
+// The backward's two products (d_in x n over d_out, d_in x d_out over n) in
+// one launch on one kind of tile, their splits folded by one more: taken when
+// the model puts it ahead of separate launches (at about 2.5 us each).
+static bool plan_joint(int64_t d_in, int64_t n, int64_t d_out, ProductPlan *px, ProductPlan *pw) {
+  double best = px->us + pw->us + 2.5;
+  bool found = false;
+  const int64_t steps_x = ceil_div(d_out, 64), steps_w = ceil_div(n, 64);
+  for (const TileCost &t : kTiles) {
+    if (t.core == k128x32 || t.core == k256x256) continue;
+    const int64_t tx = tile_count(d_in, n, t.bm, t.bn), tw = tile_count(d_in, d_out, t.bm, t.bn);
+    for (int64_t sx = 1; sx <= kMostSplits && sx <= steps_x; sx *= 2)
+      for (int64_t sw = 1; sw <= kMostSplits && sw <= steps_w; sw *= 2) {
+        const int64_t per_x = ceil_div(steps_x, sx), per_w = ceil_div(steps_w, sw);
+        if ((sx - 1) * per_x >= steps_x || (sw - 1) * per_w >= steps_w) continue;
+        const bool alone = tx * sx + tw * sw <= kComputeUnits;
+        const double step = alone ? t.step_alone : t.step_shared;
+        const double cost_x = t.round + double(per_x) * step, cost_w = t.round + double(per_w) * step;
+        double us = (double(tx * sx) * cost_x + double(tw * sw) * cost_w) / double(t.at_once);
+        const double longest = cost_x > cost_w ? cost_x : cost_w;
+        if (us < longest) us = longest;
+        us += fold_us(d_in, n, sx) + fold_us(d_in, d_out, sw) - (sx > 1 && sw > 1 ? 3.0 : 0.0);
+        if (us < best) {
+          best = us;
+          found = true;
+          *px = ProductPlan{t.core, sx, per_x * 64, partial_bytes(d_in, n, sx), us};
+          *pw = ProductPlan{t.core, sw, per_w * 64, partial_bytes(d_in, d_out, sw), us};
+        }
+      }
+  }
+  return found;
 }
 
 // The register-staged core of the losses: any alignment, 64-bit offsets.
@@ -541,6 +598,37 @@ static TileParams tile_params(const ProductPlan &pl, Operand A, Operand B, int64
   return g;
 }
 
+// Where the tiles of a planned product write, and how its splits are folded.
+static OutParams product_out(const ProductPlan &pl, int64_t M, int64_t N, const OutParams &out,
+                             char *part) {
+  if (pl.splits == 1) return out;
+  OutParams o = {};
+  o.out = part;
+  o.ld = round_to(M, 8);
+  o.rows = out.rows;
+  o.cols = out.cols;
+  o.out_f32 = 1;
+  o.split_stride = N * o.ld;
+  return o;
+}
+static FoldJob fold_job(const ProductPlan &pl, int64_t M, int64_t N, const OutParams &out,
+                        const char *part) {
+  FoldJob j = {};
+  if (pl.splits == 1) return j;
+  j.part = reinterpret_cast<const float *>(part);
+  j.ld = round_to(M, 8);
+  j.stride = N * j.ld;
+  j.splits = int32_t(pl.splits);
+  const int64_t blocks = ceil_div(j.ld / 8 * out.cols, 256);
+  j.blocks = uint32_t(blocks < 4096 ? blocks : 4096);
+  j.out = out;
+  return j;
+}
+template <bool F16>
+static void run_folds(const FoldJob &a, const FoldJob &b, hipStream_t st) {
+  if (a.blocks + b.blocks) fold_kernel<F16><<<a.blocks + b.blocks, 256, 0, st>>>(a, b);
+}
+
 // Runs a planned product of padded, aligned operands.  AK, BKM: the operand
 // is K-major (the small tiles take K-major ones only).
 // `any`: K-major operands at any alignment (not for the 256 x 256 core).
@@ -548,16 +636,7 @@ template <bool F16, bool AK, bool BKM>
 static void run_product(const ProductPlan &pl, Operand A, Operand B, int64_t M, int64_t N,
                         int64_t K, const OutParams &out, char *part, hipStream_t st,
                         bool any = false) {
-  OutParams o = out;
-  if (pl.splits > 1) {
-    o = {};
-    o.out = part;
-    o.ld = round_to(M, 8);
-    o.rows = out.rows;
-    o.cols = out.cols;
-    o.out_f32 = 1;
-    o.split_stride = N * o.ld;
-  }
+  const OutParams o = product_out(pl, M, N, out, part);
   if (pl.core == kGeneric) {
     run_generic<F16, AK, BKM>(A, B, M, N, K, out, st);
   } else if (pl.core == k256x256) {
@@ -579,11 +658,7 @@ static void run_product(const ProductPlan &pl, Operand A, Operand B, int64_t M, 
       else tile_kernel<T><<<g.blocks, T::NT, 0, st>>>(g, OutEpi<T>{o});
     });
   }
-  if (pl.splits > 1) {
-    const int64_t blocks = ceil_div(o.ld / 8 * out.cols, 256);
-    fold_kernel<F16><<<uint32_t(blocks < 4096 ? blocks : 4096), 256, 0, st>>>(
-        reinterpret_cast<const float *>(part), o.ld, o.split_stride, int(pl.splits), out);
-  }
+  run_folds<F16>(fold_job(pl, M, N, out, part), FoldJob{}, st);
 }
 
 // The tiled cores address 256 rows of an operand with 32-bit byte offsets.
@@ -598,11 +673,12 @@ struct LinearPlan {
 
 struct BackwardPlan {
   ProductPlan px, pw;                     // d_x and d_weight
+  bool joint = false;                     // both in one launch, on the same tiles
   bool mn_x = false, mn_w = false;        // operands as they lie, not transposed copies
   int64_t ld_in = 0, ld_out = 0, ld_n = 0;
   int64_t sum_parts = 0;
   size_t off_g = 0, off_gt = 0, off_x = 0, off_xt = 0, off_w = 0, off_wt = 0;
-  size_t off_part = 0, off_sums = 0, total = 0;
+  size_t off_part = 0, off_part_w = 0, off_sums = 0, total = 0;
 };
 
 struct Layout {
@@ -618,7 +694,7 @@ static int32_t plan_linear(int64_t n, int64_t d_in, int64_t d_out, int32_t dtype
   if (const int32_t st = lce_dims_check(n, d_in, d_out); st != LCE_OK) return st;
   if (!half_type(dtype)) return LCE_DTYPE_MISMATCH;
   Layout l;
-  p->product = plan_product(d_out, n, d_in);
+  p->product = plan_product(d_out, n, d_in, true);
   if (n <= kFewTokens && d_in % 8 != 0) p->product = ProductPlan{kFew};
   if (p->product.core == kFew) return LCE_OK;
   if (p->product.core == k256x256 ? d_in % 64 != 0 : d_in % 8 != 0) {
@@ -650,18 +726,18 @@ static int32_t plan_linear_backward(int64_t n, int64_t d_in, int64_t d_out, int3
   if (const int32_t st = lce_dims_check(n, d_in, d_out); st != LCE_OK) return st;
   if (!half_type(dtype)) return LCE_DTYPE_MISMATCH;
   Layout l;
-  p->px = plan_product(d_in, n, d_out);
-  if (p->px.core == kFew) p->px = ProductPlan{k64x64, 1, round_to(d_out, 64)};
-  p->pw = plan_product(d_in, d_out, n);
-  if (p->pw.core == kFew) p->pw = ProductPlan{k64x64, 1, round_to(n, 64)};
+  p->px = plan_product(d_in, n, d_out, false);
+  p->pw = plan_product(d_in, d_out, n, false);
+  p->joint = plan_joint(d_in, n, d_out, &p->px, &p->pw);
   p->ld_in = round_to(d_in, 64);
   p->ld_out = round_to(d_out, 64);
   p->ld_n = round_to(n, 64);
+  if (!offsets_fit(p->ld_out) || !offsets_fit(p->ld_n)) p->joint = false;
   if (!offsets_fit(p->ld_out)) p->px = p->pw = ProductPlan{};
   else if (!offsets_fit(p->ld_n) && p->pw.core != k256x256) {
     // (more than 4 million tokens: transposed copies would be too wide)
     p->pw = ProductPlan{k256x256, 16, round_to(ceil_div(n, 16), 64)};
-    p->pw.part_bytes = size_t(16 * d_out * round_to(d_in, 8)) * 4;
+    p->pw.part_bytes = partial_bytes(d_in, d_out, 16);
   }
   // Only the 256 x 256 core takes operands that are not K-major.  d_weight's
   // two are so as they lie and cost it nothing (8192 x 4096 x 4096: 231 us
@@ -682,7 +758,8 @@ static int32_t plan_linear_backward(int64_t n, int64_t d_in, int64_t d_out, int3
     p->off_gt = l.take(size_t(d_out * p->ld_n * 2));
     p->off_xt = l.take(size_t(d_in * p->ld_n * 2));
   }
-  p->off_part = l.take(p->px.part_bytes > p->pw.part_bytes ? p->px.part_bytes : p->pw.part_bytes);
+  p->off_part = l.take(p->px.part_bytes);
+  p->off_part_w = l.take(p->pw.part_bytes);
   p->off_sums = l.take(size_t(p->sum_parts * d_out * 4));
   p->total = l.at + 256;
   return LCE_OK;
@@ -861,25 +938,27 @@ static void linear_backward_run(const BackwardPlan &p, const lce_tensor *dy, con
     ow.add = add;
   }
   const int64_t k_x = p.px.core == k256x256 ? p.ld_out : round_to(d_out, 8);
-  if (kk_x && kk_w && p.px.core == p.pw.core && p.px.core != k256x256 && p.px.splits == 1 &&
-      p.pw.splits == 1) {
+  char *part_x = ws + p.off_part, *part_w = ws + p.off_part_w;
+  if (p.joint && kk_x && kk_w) {
     with_tile<F16>(p.px.core, [&](auto tile) {
       typedef decltype(tile) T;
       const TileParams gx = tile_params<T>(p.px, W, G, d_in, n, k_x);
       const TileParams gw = tile_params<T>(p.pw, X, GT, d_in, d_out, p.ld_n);
-      // (the deeper product first: its tiles take longest)
-      const bool w_first = p.ld_n > k_x;
+      const OutEpi<T> ex = {product_out(p.px, d_in, n, ox, part_x)};
+      const OutEpi<T> ew = {product_out(p.pw, d_in, d_out, ow, part_w)};
+      // (the tiles that take longest first)
+      const bool w_first = p.pw.k_per_split > p.px.k_per_split;
       backward_kernel<T><<<gx.blocks + gw.blocks + bias_blocks, T::NT, 0, st>>>(
-          w_first ? gw : gx, OutEpi<T>{w_first ? ow : ox}, w_first ? gx : gw,
-          OutEpi<T>{w_first ? ox : ow}, bias);
+          w_first ? gw : gx, w_first ? ew : ex, w_first ? gx : gw, w_first ? ex : ew, bias);
     });
+    run_folds<F16>(fold_job(p.px, d_in, n, ox, part_x), fold_job(p.pw, d_in, d_out, ow, part_w), st);
     return;
   }
   if (want_b) bias_grad_kernel<F16><<<bias_blocks, 256, 0, st>>>(bias);
-  if (mn_x) run_product<F16, false, true>(p.px, W, G, d_in, n, d_out, ox, ws + p.off_part, st);
-  if (kk_x) run_product<F16, true, true>(p.px, W, G, d_in, n, k_x, ox, ws + p.off_part, st);
-  if (mn_w) run_product<F16, false, false>(p.pw, X, G, d_in, d_out, n, ow, ws + p.off_part, st);
-  if (kk_w) run_product<F16, true, true>(p.pw, X, GT, d_in, d_out, p.ld_n, ow, ws + p.off_part, st);
+  if (mn_x) run_product<F16, false, true>(p.px, W, G, d_in, n, d_out, ox, part_x, st);
+  if (kk_x) run_product<F16, true, true>(p.px, W, G, d_in, n, k_x, ox, part_x, st);
+  if (mn_w) run_product<F16, false, false>(p.pw, X, G, d_in, d_out, n, ow, part_w, st);
+  if (kk_w) run_product<F16, true, true>(p.pw, X, GT, d_in, d_out, p.ld_n, ow, part_w, st);
 }
 
 }  // namespace lce
