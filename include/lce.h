@@ -33,12 +33,16 @@
  *   five calls above with out == NULL never wait: they return once their
  *   kernels are enqueued (no allocation, no memset, so they can be captured
  *   in a HIP graph), and the scalars and the verdict of the target guard
- *   reach the host through lce_loss_fetch.
+ *   reach the host through lce_loss_fetch.  The operators next to the losses
+ *   (lce_linear, lce_linear_backward, lce_pack8, lce_unpack8,
+ *   lce_beam_select, lce_beam_reorder) only enqueue kernels, too.
  * Validation order: dimensions -> chunk -> scalars -> dtypes -> buffer
  *   lengths and workspace size -> objective id -> device-side target guard
  *   -> compute.  The target guard runs on the device; when it fails, every
  *   compute kernel of that call exits before writing, and 586 is returned by
- *   the call (synchronous calls) or by the next lce_loss_fetch.
+ *   the call (synchronous calls) or by the next lce_loss_fetch.  The
+ *   operators next to the losses check dimensions -> dtypes -> lengths and
+ *   workspace -> activation or end id, all on the host.
  * Precision: bf16 and fp16 inputs are multiplied on the matrix cores with
  *   fp32 accumulation; every softmax statistic is fp32 and every token sum
  *   fp64.  fp64 inputs run end to end in fp64.  16-bit gradients (d_hidden,
@@ -61,9 +65,9 @@ extern "C" {
 #define LCE_DIMENSION_TOO_LARGE 583          /* a dimension above its ceiling       */
 #define LCE_WORK_BUDGET_EXCEEDED 584         /* n_tok*d_model*vocab > 2^46          */
 #define LCE_NON_FINITE_SCALAR 585            /* NaN/Inf scalar, or temperature <= 0 */
-#define LCE_TARGET_OUT_OF_RANGE 586          /* a target id < 0 or >= vocab         */
+#define LCE_TARGET_OUT_OF_RANGE 586          /* a target or end id outside vocab    */
 #define LCE_CHUNK_EXCEEDS_LOGIT_BUDGET 587   /* chunk*vocab > 2^27                  */
-#define LCE_UNKNOWN_OBJECTIVE 588            /* distillation objective id not 0..2  */
+#define LCE_UNKNOWN_OBJECTIVE 588            /* distillation objective or activation*/
 #define LCE_DEVICE_ERROR 589                 /* extension: a HIP call failed        */
 #define LCE_DTYPE_MISMATCH 590               /* extension: unsupported dtype combo  */
 
