@@ -363,6 +363,26 @@ __global__ void __launch_bounds__(T::NT) backward_kernel(TileParams g0, OutEpi<T
   bias_grad_block<T::F16>(bias, b - g1.blocks, reinterpret_cast<float *>(smem));
 }
 
+// The large backward in one launch: d_weight's tiles (operands as they lie),
+// d_x's (K-major) and the bias gradient's sums.  One product's tail and its
+// stores run beside the other's tiles (8192 x 4096 x 4096: 537 us for the call,
+// 549 with three launches on the same box).
+template <bool F16>
+__global__ void __launch_bounds__(TraitsH16W8<F16>::NT) big_backward_kernel(
+    Gemm2Params gw, OutEpi<TraitsH16W8<F16>> ew, uint32_t blocks_w, Gemm2Params gx,
+    OutEpi<TraitsH16W8<F16>> ex, uint32_t blocks_x, BiasGrad bias) {
+  typedef TraitsH16W8<F16> TR;
+  typedef PipeCfg<64, 2> CFG;
+  __shared__ __attribute__((aligned(1024))) char smem[gemm2_lds_bytes<CFG, OutEpi<TR>>()];
+  const uint32_t b = blockIdx.x;
+  if (b < blocks_w)
+    big_block<CFG, TR, false, false, OutEpi<TR>>(gw, ew, b, blocks_w, smem);
+  else if (b - blocks_w < blocks_x)
+    big_block<CFG, TR, true, true, OutEpi<TR>>(gx, ex, b - blocks_w, blocks_x, smem);
+  else
+    bias_grad_block<F16>(bias, b - blocks_w - blocks_x, reinterpret_cast<float *>(smem));
+}
+
 // Adds the K-splits ([split][cols][ld] fp32) of one or two products in order
 // and finishes.
 struct FoldJob {
@@ -598,6 +618,17 @@ static TileParams tile_params(const ProductPlan &pl, Operand A, Operand B, int64
   return g;
 }
 
+static Gemm2Params big_params(const ProductPlan &pl, Operand A, Operand B, int64_t M, int64_t N,
+                              int64_t K) {
+  Gemm2Params g = {};
+  g.A = A.p; g.lda = A.ld; g.B = B.p; g.ldb = B.ld;
+  g.M = M; g.N = N; g.K = K;
+  g.M_read = A.ld; g.N_read = B.ld;
+  g.k_per_split = pl.k_per_split;
+  g.tiles_n = ceil_div(N, 256);
+  return g;
+}
+
 // Where the tiles of a planned product write, and how its splits are folded.
 static OutParams product_out(const ProductPlan &pl, int64_t M, int64_t N, const OutParams &out,
                              char *part) {
@@ -642,12 +673,7 @@ static void run_product(const ProductPlan &pl, Operand A, Operand B, int64_t M, 
   } else if (pl.core == k256x256) {
     typedef TraitsH16W8<F16> TR;
     typedef PipeCfg<64, 2> CFG;
-    Gemm2Params g = {};
-    g.A = A.p; g.lda = A.ld; g.B = B.p; g.ldb = B.ld;
-    g.M = M; g.N = N; g.K = K;
-    g.M_read = A.ld; g.N_read = B.ld;
-    g.k_per_split = pl.k_per_split;
-    g.tiles_n = ceil_div(N, 256);
+    const Gemm2Params g = big_params(pl, A, B, M, N, K);
     const int64_t wgs = tile_count(M, N, 256, 256) * pl.splits;
     big_kernel<CFG, TR, AK, BKM, OutEpi<TR>><<<uint32_t(wgs), TR::NT, 0, st>>>(g, OutEpi<TR>{o});
   } else if constexpr (AK && BKM) {
@@ -951,6 +977,18 @@ static void linear_backward_run(const BackwardPlan &p, const lce_tensor *dy, con
       backward_kernel<T><<<gx.blocks + gw.blocks + bias_blocks, T::NT, 0, st>>>(
           w_first ? gw : gx, w_first ? ew : ex, w_first ? gx : gw, w_first ? ex : ew, bias);
     });
+    run_folds<F16>(fold_job(p.px, d_in, n, ox, part_x), fold_job(p.pw, d_in, d_out, ow, part_w), st);
+    return;
+  }
+  if (kk_x && mn_w && p.px.core == k256x256 && p.pw.core == k256x256) {
+    typedef TraitsH16W8<F16> TR;
+    const uint32_t bx = uint32_t(tile_count(d_in, n, 256, 256) * p.px.splits);
+    const uint32_t bw = uint32_t(tile_count(d_in, d_out, 256, 256) * p.pw.splits);
+    big_backward_kernel<F16><<<bw + bx + bias_blocks, TR::NT, 0, st>>>(
+        big_params(p.pw, X, G, d_in, d_out, n),
+        OutEpi<TR>{product_out(p.pw, d_in, d_out, ow, part_w)}, bw,
+        big_params(p.px, W, G, d_in, n, k_x), OutEpi<TR>{product_out(p.px, d_in, n, ox, part_x)},
+        bx, bias);
     run_folds<F16>(fold_job(p.px, d_in, n, ox, part_x), fold_job(p.pw, d_in, d_out, ow, part_w), st);
     return;
   }

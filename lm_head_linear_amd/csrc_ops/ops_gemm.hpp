@@ -366,16 +366,21 @@ __device__ inline uint32_t xcd_order(uint32_t b, uint32_t nb) {
   return xcd < r ? xcd * (q + 1) + idx : r * (q + 1) + (xcd - r) * q + idx;
 }
 
-// The 256 x 256 core in that order.
+// The 256 x 256 core in that order; workgroup `bid` of `blocks`.
 template <class CFG, class TR, bool AK, bool BKM, class Epi>
-__global__ void __launch_bounds__(TR::NT) big_kernel(Gemm2Params g, Epi epi) {
-  __shared__ __attribute__((aligned(1024))) char smem[gemm2_lds_bytes<CFG, Epi>()];
-  const uint32_t LS = xcd_order(blockIdx.x, gridDim.x);
+__device__ __forceinline__ void big_block(const Gemm2Params &g, const Epi &epi, uint32_t bid,
+                                          uint32_t blocks, char *smem) {
+  const uint32_t LS = xcd_order(bid, blocks);
   const uint32_t tiles_m = uint32_t((g.M + CFG::BM - 1) / CFG::BM), tiles_n = uint32_t(g.tiles_n);
   const uint32_t tiles = tiles_m * tiles_n, split = LS / tiles;
   uint32_t m, n;
   tile_at(LS - split * tiles, tiles_m, tiles_n, m, n);
   gemm2_tile<CFG, TR, AK, BKM, Epi>(g, epi, int64_t(split * tiles + m * tiles_n + n), smem);
+}
+template <class CFG, class TR, bool AK, bool BKM, class Epi>
+__global__ void __launch_bounds__(TR::NT) big_kernel(Gemm2Params g, Epi epi) {
+  __shared__ __attribute__((aligned(1024))) char smem[gemm2_lds_bytes<CFG, Epi>()];
+  big_block<CFG, TR, AK, BKM, Epi>(g, epi, blockIdx.x, gridDim.x, smem);
 }
 
 // One tile of one split; `bid` of `blocks` workgroups.
