@@ -21,6 +21,13 @@
 // different.
 // A second kernel, one block per sequence, folds the pieces' sums in fp64 and
 // ranks the candidates of all beams by the same kind of threshold.
+//
+// Measured: 512 x 151936 bf16, n_out 16: 37 us for the pieces (4.2 TB/s; the
+// vector units are busy 25 us of it: widening, maximum, exponential, and the
+// bit mask of what reaches T), 8.4 for the 64 sequences' merge, which is bound
+// by the latency of its four dependent reads.  64 logits a thread as they lie
+// in memory are 32 registers, so eight waves a SIMD keep loads in flight;
+// held as fp32 they left three and took 51 us.
 #include <math.h>
 
 #include <algorithm>
@@ -528,7 +535,8 @@ struct StateList {
 // no beam.  A thread owns one 16-byte column of a sequence's rows and loads
 // it for every destination before it stores any, so src may be dst; there a
 // row that stays is neither read nor written.  Bound by memory: each source
-// row that has a child is read once (its other children find it in cache).
+// row that has a child is read once (its other children find it in cache);
+// 64 rows of 16 caches [8][777 of 1024][128] bf16, 2.7 GB: 498 us, 5.4 TB/s.
 template <int B>
 __global__ void __launch_bounds__(256) beam_reorder_kernel(
     StateList list, const int64_t *parents, int64_t n_seq, int beams, int n_out, int64_t segs,

@@ -8,7 +8,8 @@
 // is the one to e4m3.
 // Bound by memory: 2 + 1 + 1/32 bytes a value each way.  A lane holds 8 values
 // (one 16-byte load); the four lanes of a quad share a block, so the maximum
-// is two lane swaps within the quad and no value leaves its lane.
+// is two lane swaps within the quad and no value leaves its lane.  8192 x 4096
+// bf16: 20 us packed, 17.5 read back (5.1 and 5.8 TB/s; a large copy: 5.0).
 #include "ops_common.h"
 
 namespace lce {
