@@ -22,12 +22,11 @@
 // A second kernel, one block per sequence, folds the pieces' sums in fp64 and
 // ranks the candidates of all beams by the same kind of threshold.
 //
-// Measured: 512 x 151936 bf16, n_out 16: 37 us for the pieces (4.2 TB/s; the
-// vector units are busy 25 us of it: widening, maximum, exponential, and the
-// bit mask of what reaches T), 8.4 for the 64 sequences' merge, which is bound
-// by the latency of its four dependent reads.  64 logits a thread as they lie
-// in memory are 32 registers, so eight waves a SIMD keep loads in flight;
-// held as fp32 they left three and took 51 us.
+// Measured: 512 x 151936 bf16: 36 us for the pieces (4.3 TB/s: the read, and
+// vector work that an earlier form's counters put at about 25 us), 8.6 for the
+// 64 sequences' merge, too little work to be more than latency.  64 logits a
+// thread as they lie in memory leave room for eight waves a SIMD (50
+// registers); held as fp32 they took 200 registers and 75 us.
 #include <math.h>
 
 #include <algorithm>

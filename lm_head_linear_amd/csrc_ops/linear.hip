@@ -18,9 +18,10 @@
 //
 // Measured (bf16, one box, us a call; a library product alone takes 212):
 // 8192 x 4096 -> 4096 with bias, gelu, residual and pre-activation 255, 1.08
-// PFLOP/s: bound by the matrix cores, then by the epilogue's 201 MB, which all
-// compute units move at the same time (about 20 us a round of tiles); its
-// backward from 8-bit checkpoints 511: 74 us of copies, 437 of products.
+// PFLOP/s: bound by the matrix cores (2 rounds of 64 steps of 1.59 us) and the
+// epilogue's 201 MB, which all compute units move at the same time; its
+// backward from 8-bit checkpoints 511 (traced: copies 79, products 489, medians
+// of calls with gaps between them, which run slower than calls in a row).
 #include <math.h>
 
 #include <numeric>
@@ -39,11 +40,11 @@ namespace lce {
 // current ones are used.  Where d_out is small, KW waves of a block share 16
 // rows, each a range of k, and their sums meet in LDS.  No alignment is asked
 // for: vector loads take any address.
-// Measured: one token 1024 x 1024 4.6 us (a launch), 4096 x 4096 8.3 us (4.1
-// TB/s), 32768 x 4096 45 us (5.9 TB/s); 32 and 64 tokens 2.9 and 1.9 TB/s, for
-// X then takes two and four times W's share of the vector memory pipe, so
-// larger heads of more than 16 tokens go to tiles (151936 x 1024, 32 tokens:
-// 60 us, 5.4 TB/s, against 111).
+// Measured, W not in a cache: one token 1024 x 1024 4.4 us (a launch), 4096 x
+// 4096 9.9 us (3.4 TB/s).  More tokens read more of X beside W (32768 x 4096,
+// one W over and over: 93 us with 32 tokens, 146 with 64, against 53 and 55 in
+// tiles), so large heads go to tiles: 151936 x 1024, 32 tokens, 60 us (5.2
+// TB/s) against 111.
 typedef float f32x4v __attribute__((ext_vector_type(4)));
 template <bool F16>
 __device__ inline f32x4v mfma16(u32x4 a, u32x4 b, f32x4v c) {
@@ -157,9 +158,9 @@ __global__ void __launch_bounds__(512) few_tokens_kernel(const uint16_t *x, cons
 // matrix into the padded row-major copy (columns behind the last are zero up
 // to ld) and / or the padded transposed one, multiplying by the activation's
 // slope and summing columns on the way where asked.
-// Bound by memory beside gelu's slope (26 us of arithmetic there): 8192 x 4096
-// from 8-bit checkpoints with W's transposed copy, 337 MB, 74 us (4.6 TB/s);
-// 64 x 256 tiles took 88, one job after the other 82.
+// Bound by memory and by the arithmetic of gelu's slope together: 8192 x 4096
+// from 8-bit checkpoints with W's transposed copy, 337 MB, 79 us (4.3 TB/s; 74
+// at best); one job after the other 92, and 64 x 256 tiles 96.
 struct CopyJob {
   const void *src;          // [rows][cols], 16-bit, or e4m3 codes with scales
   const uint8_t *scales;
@@ -360,9 +361,9 @@ __global__ void __launch_bounds__(256) bias_grad_kernel(BiasGrad a) {
 }
 
 // The small backward in one launch: two products on the same tiles and the
-// bias gradient's sums, which need nothing of each other (515 x 1003 -> 777:
-// 18.4 us for the call, 26.3 with a launch each).  Bound by the latency of the
-// tiles' steps, about 0.3 us each.
+// bias gradient's sums, which need nothing of each other (515 x 1003 -> 777: the
+// call took 26.3 us with a launch each, 19.4 with one and 32-bit tile numbers).
+// Bound by the latency of the tiles' steps, about 0.3 us each.
 template <class T>
 __global__ void __launch_bounds__(T::NT) backward_kernel(TileParams g0, OutEpi<T> e0, TileParams g1,
                                                          OutEpi<T> e1, BiasGrad bias) {
@@ -401,8 +402,7 @@ __global__ void __launch_bounds__(TraitsH16W8<F16>::NT) big_backward_kernel(
 }
 
 // Adds the K-splits ([split][cols][ld] fp32) of one or two products in order
-// and finishes.  Bound by the read of the partial results, which mostly are
-// still in the caches.
+// and finishes.  Its cost is a launch and the partial results' read (fold_us).
 struct FoldJob {
   const float *part;
   int64_t ld, stride;
@@ -858,7 +858,8 @@ static void linear_run(const LinearPlan &p, const lce_tensor *x, const lce_tenso
   if (p.product.core == kFew || (n <= kFewTokens && !aligned)) {
     const int64_t groups = ceil_div(d_out, 16);
     // waves that share 16 rows, with 128 k each at least (1024 x 1024, one
-    // token: 7.4, 6.0, 4.8, 4.9 us with 1, 2, 4, 8; 4096 x 4096: 20, 12, 8.3, 8.2)
+    // token, W in a cache: 7.4, 6.0, 4.8, 4.9 us with 1, 2, 4, 8; 4096 x 4096:
+    // 20, 12, 8.3, 8.2)
     const int most = groups <= 128 ? 8 : 4;
     int kw = 1;
     while (kw < most && d_in / (2 * kw) >= 128) kw *= 2;

@@ -10,11 +10,11 @@
 // last k and rows behind the last row are fetched from behind the buffer's
 // end, which reads as zero.
 //
-// What bounds it: alone on its compute unit a 64 x 64 tile's step takes 0.34 us
-// whatever the ring's depth (5 and 9 stages tried), the number of fragments
-// read ahead or the split of the step over the waves, so the latency of wait,
-// barrier, LDS and products; two tiles a compute unit hide it until the LDS and
-// L2 traffic of small tiles does (0.41 us a step: 20 TB/s from L2).
+// What bounds it: fitted over sweeps of the depth, a 64 x 64 tile's step takes
+// 0.34 us alone on its compute unit and 0.41 beside a second.  A deeper ring (5
+// and 9 stages), all fragments read ahead (3 to 5 %) and the step split over
+// the waves changed little; which part of the step's chain of wait, barrier, LDS
+// reads and products sets it has not been separated.
 #pragma once
 
 #include "../csrc/lce_gemm2.hpp"
@@ -471,9 +471,9 @@ __global__ void __launch_bounds__(T::NT) tile_kernel(TileParams g, Epi epi) {
 // The same tile of operands at any alignment: vector loads to registers, two
 // or four stages ahead, and from there to LDS (the DMA needs aligned rows, so
 // it would take a padded copy of both operands first).  Vector loads off a
-// 16-byte boundary bound it: a step takes 0.2 to 0.4 us more than an aligned
-// one; reading whole words and shifting took longer still (15.1 us against
-// 11.7 for 515 x 1003 -> 777).
+// 16-byte boundary cost it: 777 x K -> 1531 takes 10.2 us at K = 1008 on the
+// DMA tiles, here 13.9 at 1002 and 16.6 at 1003.  Whole words and a shift took
+// longer (515 x 1003 -> 777: 15.1 us against 11.7).
 template <class T, int ROWS>
 struct AnyOperand {
   static constexpr int N = ROWS * 8 / T::NT;      // 16-byte chunks per thread
