@@ -41,7 +41,7 @@ namespace lce {
 // rows, each a range of k, and their sums meet in LDS.  No alignment is asked
 // for: vector loads take any address.
 // Measured, W not in a cache: one token 1024 x 1024 4.4 us (a launch), 4096 x
-// 4096 9.9 us (3.4 TB/s).  More tokens read more of X beside W (32768 x 4096,
+// 4096 9.9 us (3.4 TB/s), 32768 x 4096 46 us (5.8 TB/s).  More tokens read more of X beside W (32768 x 4096,
 // one W over and over: 93 us with 32 tokens, 146 with 64, against 53 and 55 in
 // tiles), so large heads go to tiles: 151936 x 1024, 32 tokens, 60 us (5.2
 // TB/s) against 111.
@@ -498,6 +498,7 @@ static double fold_us(int64_t M, int64_t N, int64_t splits) {
 static ProductPlan plan_product(int64_t M, int64_t N, int64_t K, bool few) {
   ProductPlan best;
   double best_us = 1e30;
+  int64_t best_tiles = 0;
   const int64_t steps = ceil_div(K, 64);
   const double memory_us = 2.0 * double(K) * double(M + N) / kBytesPerUs;
   for (const TileCost &t : kTiles) {
@@ -516,18 +517,32 @@ static ProductPlan plan_product(int64_t M, int64_t N, int64_t K, bool few) {
         best_us = us;
         best.core = t.core;
         best.splits = sp;
+        best_tiles = all;
         best.k_per_split = per * 64;
       }
     }
   }
   best.part_bytes = partial_bytes(M, N, best.splits);
   best.us = best_us;
-  // up to 64 rows may stream A instead: bound by the read of A, at a rate that
-  // falls with the rows that share a wave (4.8, 2.9 and 1.9 TB/s measured for
-  // up to 16, 32 and 64 rows of 32768 x 4096), with no ring to fill first
-  if (few && N <= kFewTokens) {
-    const double floor_us = N <= 16 ? 4.8 : N <= 32 ? 5.7 : 7.5;
-    const double rate = N <= 16 ? 4.8e6 : N <= 32 ? 2.9e6 : 1.9e6;
+  // Up to 64 rows may stream A instead, with no ring to fill first: bound by the
+  // read of A, at a rate that falls with the rows that share a wave.  Up to 16
+  // rows both sides are lines measured with A not in a cache, where a step of
+  // tiles that do not fill the chip takes 0.5 us: 32768 x 4096 takes 46, 54 and
+  // 67 us with 1, 8 and 16 tokens (tiles 59 with each), 151936 x 1024 50, 63 and
+  // 75 (tiles 52, 55, 57).  Fitted over 17 layers, and checked on nine others
+  // with 1 to 14 tokens: 0.3 % over the better side on average, where 4.8 TB/s
+  // for all and warm tile steps cost 2.3 %.  Beyond 16: 2.9 and 1.9 TB/s for up
+  // to 32 and 64 rows, from one A read over and over.
+  if (few && N <= 16) {
+    const double cold_us = 1.5 + 0.5 * double(best.k_per_split / 64) + (best.splits > 1 ? 3.0 : 0.0);
+    if (best_tiles <= kComputeUnits && best_us < cold_us) best_us = cold_us;
+    const double us = 2.0 + 2.0e-6 * double(M) * double(K) * (0.165 + 0.007 * double(N - 1));
+    if ((us > 4.8 ? us : 4.8) < best_us) {
+      best = ProductPlan{};
+      best.core = kFew;
+    }
+  } else if (few && N <= kFewTokens) {
+    const double floor_us = N <= 32 ? 5.7 : 7.5, rate = N <= 32 ? 2.9e6 : 1.9e6;
     const double us = 2.0 + 2.0 * double(M) * double(K) / rate;
     if ((us > floor_us ? us : floor_us) < best_us + 2.5) {
       best = ProductPlan{};
