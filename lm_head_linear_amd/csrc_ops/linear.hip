@@ -799,9 +799,10 @@ static int32_t plan_linear_backward(int64_t n, int64_t d_in, int64_t d_out, int3
     p->pw.part_bytes = partial_bytes(d_in, d_out, 16);
   }
   // Only the 256 x 256 core takes operands that are not K-major.  d_weight's
-  // two are so as they lie and cost it nothing (8192 x 4096 x 4096: 231 us
-  // against 225 K-major); d_x's W beside K-major G costs a fifth (286 us), more
-  // than W's transposed copy unless few tokens share it.
+  // two are so as they lie and cost it less than copies would (8192 x 4096 x
+  // 4096, traced: least 227 to 231 us, median 265 to 277, against d_x's 228 to
+  // 233 and 245 to 252 K-major); d_x's W beside K-major G costs a fifth (least
+  // 287, median 316), more than W's transposed copy unless few tokens share it.
   const double step_cost = 0.3 * double(ceil_div(tile_count(d_in, n, 256, 256), 256)) *
                            double(ceil_div(d_out, 64));
   p->mn_w = p->pw.core == k256x256 || p->pw.core == kGeneric;
