@@ -499,7 +499,9 @@ int64_t lce_beam_workspace_bytes(int64_t n_seq, int64_t beams, int64_t vocab, in
  * beam k (lse_k their log-sum-exp), the n_out largest totals of a sequence's
  * beams x vocab, best first, equal ones by the lower beam, then the lower
  * token.  Each beam competes with its n_out largest logits (equal ones by the
- * lower token); totals are formed and compared in fp64.
+ * lower token); totals are formed and compared in fp64, the largest logit
+ * subtracted before the logarithm of the sum, so that any finite logits (a
+ * vocabulary masked by the type's lowest number) keep their order.
  *   logits       [n_seq*beams*vocab] LCE_BF16, LCE_F16 or LCE_F32
  *   scores       [n_seq*beams] LCE_F32, the beams' accumulated scores
  *   finished     [n_seq*beams] LCE_U8 or data == NULL: a beam with nonzero
@@ -515,7 +517,8 @@ int64_t lce_beam_workspace_bytes(int64_t n_seq, int64_t beams, int64_t vocab, in
  * A beam offers nothing when its score is not finite, when no token with a
  * logit above -inf is allowed, or when an allowed logit is NaN or +inf.  A
  * sequence with fewer than n_out candidates ends in entries of score -inf,
- * parent -1 and token -1.  Only enqueues on `stream`; statuses as
+ * parent -1 and token -1.  A total below fp32's range is written as -inf, with
+ * its parent and token.  Only enqueues on `stream`; statuses as
  * lce_beam_workspace_bytes, 590 for a dtype, 582 for a short buffer. */
 int32_t lce_beam_select(const lce_tensor *logits, const lce_tensor *scores,
                         const lce_tensor *finished, const lce_tensor *allowed, int64_t n_seq,

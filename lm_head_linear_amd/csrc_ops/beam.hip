@@ -244,9 +244,11 @@ __global__ void __launch_bounds__(kBeamThreads, sizeof(typename Logit<T>::E) == 
   __syncthreads();
   top = fmaxf(fmaxf(s_top[0], s_top[1]), fmaxf(s_top[2], s_top[3]));
   const float m = top == -INFINITY ? 0.0f : top;
-  // exp(x - m) = 2^(x L - m L): m L as the rounded hi that the fma subtracts
-  // and an exact rest that scales the sum
-  const float L2E = 1.4426950408889634f, hi = m * L2E, lo = fmaf(m, L2E, -hi);
+  // exp(x - m) = 2^((x - m) log2 e): the difference first, so that it is 0 at
+  // the maximum and at most 0 elsewhere however large the logits are (m log2 e
+  // subtracted from x log2 e by an fma leaves m's own rounding, which passes
+  // 2^7 from |m| of about 3e9 on)
+  const float L2E = 1.4426950408889634f;
   float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
   for (int v = 0; v < VECS; ++v) {
@@ -254,7 +256,7 @@ __global__ void __launch_bounds__(kBeamThreads, sizeof(typename Logit<T>::E) == 
     Logit<T>::hold(x[v]);
     Logit<T>::values(x[v], f);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) sum[i & 3] += __builtin_amdgcn_exp2f(fmaf(f[i], L2E, -hi));
+    for (int i = 0; i < 8; ++i) sum[i & 3] += __builtin_amdgcn_exp2f((f[i] - m) * L2E);
     __builtin_amdgcn_sched_barrier(0);      // (widened values of one vector at a time)
   }
   const double wsum = wave_sum_rows((sum[0] + sum[1]) + (sum[2] + sum[3]));
@@ -293,7 +295,7 @@ __global__ void __launch_bounds__(kBeamThreads, sizeof(typename Logit<T>::E) == 
   __syncthreads();
   if (tid == 0) {
     PieceStats st;
-    st.sum = (((s_sum[0] + s_sum[1]) + s_sum[2]) + s_sum[3]) * double(__builtin_amdgcn_exp2f(-lo));
+    st.sum = ((s_sum[0] + s_sum[1]) + s_sum[2]) + s_sum[3];
     st.top = top;
     st.pad = 0;
     stats[int64_t(row) * pieces + piece] = st;
@@ -367,8 +369,9 @@ __global__ void __launch_bounds__(kBeamThreads) beam_merge_kernel(
     int64_t *out_tokens, uint8_t *out_finished) {
   const int64_t seq = blockIdx.x;
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  __shared__ double s_shift[kMaxBeams];     // score - lse, or the score of a finished beam
-  __shared__ double s_lse[kMaxBeams];
+  // A total is score + ((x - top) - log_sum): the maximum goes first, so that
+  // a large one does not swallow the logarithm.
+  __shared__ double s_score[kMaxBeams], s_top[kMaxBeams], s_log_sum[kMaxBeams];
   __shared__ int s_state[kMaxBeams];        // 0: offers nothing, 1: open, 2: finished
   __shared__ uint64_t s_total[kBeamList];
   __shared__ uint32_t s_place[kBeamList];
@@ -411,13 +414,13 @@ __global__ void __launch_bounds__(kBeamThreads) beam_merge_kernel(
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor(sum, o);
     }
-    const double m = top == -INFINITY ? 0.0 : double(top);
     if ((tid & 31) == 0) {
-      const double lse = m + log(sum);
-      s_lse[k] = done ? 0.0 : lse;
-      s_shift[k] = score;
-      // NaN, +inf or nothing allowed: the beam offers nothing
-      s_state[k] = !isfinite(score) ? 0 : done ? 2 : isfinite(lse) ? 1 : 0;
+      const double log_sum = log(sum);
+      s_score[k] = score;
+      s_top[k] = top;
+      s_log_sum[k] = log_sum;
+      // NaN, +inf (whose sum is NaN) or nothing allowed: the beam offers nothing
+      s_state[k] = !isfinite(score) ? 0 : done ? 2 : isfinite(log_sum) ? 1 : 0;
     }
   }
   if (tid == 0) s_count = 0;
@@ -430,7 +433,8 @@ __global__ void __launch_bounds__(kBeamThreads) beam_merge_kernel(
       for (int u = 0; u < 8; ++u) {
         const uint32_t k = uint32_t(i0 + u * kBeamThreads) / uint32_t(per_beam);
         if (key[u] != 0 && k < uint32_t(beams) && s_state[k] == 1)
-          use(BeamKey{order64(s_shift[k] + (double(unorder32(uint32_t(key[u] >> 32))) - s_lse[k])),
+          use(BeamKey{order64(s_score[k] + ((double(unorder32(uint32_t(key[u] >> 32))) - s_top[k]) -
+                                            s_log_sum[k])),
                       (k << 24) | ~uint32_t(key[u])});
       }
     };
@@ -445,7 +449,7 @@ __global__ void __launch_bounds__(kBeamThreads) beam_merge_kernel(
       look(key, i0);
     }
     if (tid < beams && s_state[tid] == 2)
-      use(BeamKey{order64(s_shift[tid]), (uint32_t(tid) << 24) | uint32_t(eos)});
+      use(BeamKey{order64(s_score[tid]), (uint32_t(tid) << 24) | uint32_t(eos)});
   };
   uint32_t best = 0;      // the leading half of the largest total
   each([&](const BeamKey &c) {
