@@ -42,6 +42,13 @@ void need(bool ok, const char *what) {
   if (!ok) throw py::value_error(what);
 }
 
+// A tensor that was given has to have the shape, not only the elements: one in
+// another order would be read or written wrongly.
+bool fits(const MaybeTensor &t, int64_t rows, int64_t cols) {
+  return !t || (t->dim() == 2 && t->size(0) == rows && t->size(1) == cols);
+}
+int64_t pack8_blocks(int64_t d) { return (d + LCE_PACK8_BLOCK - 1) / LCE_PACK8_BLOCK; }
+
 // The descriptor of a contiguous tensor on the GPU of the call.
 struct On {
   c10::Device device;
@@ -78,7 +85,7 @@ py::tuple pack8(const Tensor &x) {
   const c10::DeviceGuard guard(on.device);
   const int64_t n = x.size(0), d = x.size(1);
   Tensor codes = on.empty({n, d}, at::kByte);
-  Tensor scales = on.empty({n, (d + LCE_PACK8_BLOCK - 1) / LCE_PACK8_BLOCK}, at::kByte);
+  Tensor scales = on.empty({n, pack8_blocks(d)}, at::kByte);
   const lce_tensor tx = on(x);
   lce_tensor tc = on(codes), ts = on(scales);
   const int32_t st = lce_pack8(&tx, n, d, &tc, &ts, on.stream());
@@ -135,6 +142,14 @@ py::tuple linear_backward(const Tensor &d_out_grad, const MaybeTensor &x, const 
   const int64_t d_in = weight ? weight->size(1) : x->size(1);
   need((!x || (x->size(0) == n && x->size(1) == d_in)) && (!weight || weight->size(0) == m),
        "x or weight does not fit d_out");
+  // (what is not read or written may have any shape)
+  const bool slope = activation != LCE_ACT_NONE;
+  need(!slope || fits(preact, n, m), "preact does not fit d_out");
+  need((!want_weight || fits(x_scales, n, pack8_blocks(d_in))) &&
+           (!slope || fits(preact_scales, n, pack8_blocks(m))),
+       "scales do not fit their codes");
+  need(!want_weight || fits(d_weight_in, m, d_in), "d_weight does not fit weight");
+  need(!want_bias || !d_bias_in || d_bias_in->numel() == m, "d_bias does not fit d_out");
   need(!accumulate || ((!want_weight || d_weight_in) && (!want_bias || d_bias_in)),
        "accumulate needs the gradients it adds to");
   const On on(d_out_grad);

@@ -736,8 +736,10 @@ def linear_backward(d_out, x, weight, preact=None, activation="none", want_x=Tru
     """Gradients of linear(): allocate those wanted (d_weight in
     weight_grad_dtype, fp32 unless given, d_bias in fp32) and (if needed) the
     workspace, call lce_linear_backward.  x and preact may each be a Packed8;
-    x may be None without want_weight, weight without want_x.  d_weight and
-    d_bias may be given, and are added to with accumulate."""
+    x may be None without want_weight, weight without want_x.  d_weight
+    [d_out][d_in] and d_bias [d_out] may be given, and are added to with
+    accumulate.  What is read or written has to have its shape, preact
+    d_out's (ValueError)."""
     xs = zs = None
     if isinstance(x, Packed8):
         x, xs = x.codes, x.scales
