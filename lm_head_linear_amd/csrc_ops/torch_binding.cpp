@@ -176,6 +176,13 @@ py::tuple beam_select(const Tensor &logits, const Tensor &scores, int64_t n_out,
   need(logits.dim() == 2 && scores.dim() == 2, "logits and scores must be two-dimensional");
   const int64_t n_seq = scores.size(0), beams = scores.size(1), vocab = logits.size(1);
   need(logits.size(0) == n_seq * beams, "logits need one row per beam");
+  need(!finished || fits(finished, n_seq, beams) ||
+           (finished->dim() == 1 && finished->size(0) == n_seq * beams),
+       "finished does not fit scores");
+  need(!allowed || fits(allowed, n_seq * beams, vocab) ||
+           (allowed->dim() == 3 && allowed->size(0) == n_seq && allowed->size(1) == beams &&
+            allowed->size(2) == vocab),
+       "allowed does not fit logits");
   const On on(logits);
   const c10::DeviceGuard guard(on.device);
   const lce_tensor tl = on(logits), ts = on(scores), tf = on(finished), ta = on(allowed);

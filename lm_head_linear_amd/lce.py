@@ -651,7 +651,9 @@ class BeamStep:
 def beam_select(logits, scores, n_out, finished=None, allowed=None, eos=None,
                 workspace=None) -> BeamStep:
     """Allocate the outputs and (if needed) the workspace, call lce_beam_select
-    for logits [n_seq*beams][vocab] and scores [n_seq][beams]."""
+    for logits [n_seq*beams][vocab] and scores [n_seq][beams].  finished is
+    shaped as scores or [n_seq*beams], allowed as logits or
+    [n_seq][beams][vocab] (ValueError otherwise)."""
     st, best, parents, tokens, done = _torch_calls().beam_select(
         logits, scores, n_out, finished, allowed, -1 if eos is None else eos, workspace)
     _check(st, "lce_beam_select")

@@ -75,3 +75,28 @@ def test_backward_given_d_weight_shape(shape):
 def test_backward_given_d_bias_shape(numel):
     with pytest.raises(ValueError, match="d_bias"):
         _backward(d_bias=torch.zeros(numel))
+
+
+def _select(**kw):
+    base = dict(logits=torch.zeros(6, 50), scores=torch.zeros(2, 3), n_out=3, eos=1)
+    return lce.beam_select(**{**base, **kw})
+
+
+def test_select_shapes_that_fit_reach_the_device_check():
+    for kw in ({"finished": torch.zeros(2, 3, dtype=U8)}, {"finished": torch.zeros(6, dtype=U8)},
+               {"allowed": torch.ones(6, 50, dtype=U8)}, {"allowed": torch.ones(2, 3, 50, dtype=U8)}):
+        with pytest.raises(ValueError, match="GPU"):
+            _select(**kw)
+
+
+@pytest.mark.parametrize("shape", [(3, 2), (5,), (7,), (6, 1), (1, 6), (2, 4), (2, 3, 1)])
+def test_select_finished_shape(shape):
+    with pytest.raises(ValueError, match="finished"):
+        _select(finished=torch.zeros(shape, dtype=U8))
+
+
+@pytest.mark.parametrize("shape", [(50, 6), (300,), (6, 51), (7, 50), (3, 2, 50), (2, 3, 51),
+                                   (50, 2, 3), (2, 150), (50,)])
+def test_select_allowed_shape(shape):
+    with pytest.raises(ValueError, match="allowed"):
+        _select(allowed=torch.ones(shape, dtype=U8))
