@@ -94,6 +94,7 @@ py::tuple pack8(const Tensor &x) {
 
 py::tuple unpack8(const Tensor &codes, const Tensor &scales, at::ScalarType dtype) {
   need(codes.dim() == 2, "codes must be two-dimensional");
+  need(fits(scales, codes.size(0), pack8_blocks(codes.size(1))), "scales do not fit their codes");
   const On on(codes);
   const c10::DeviceGuard guard(on.device);
   const int64_t n = codes.size(0), d = codes.size(1);

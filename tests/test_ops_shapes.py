@@ -100,3 +100,11 @@ def test_select_finished_shape(shape):
 def test_select_allowed_shape(shape):
     with pytest.raises(ValueError, match="allowed"):
         _select(allowed=torch.ones(shape, dtype=U8))
+
+
+@pytest.mark.parametrize("shape,fits", [((N, 3), True), ((3, N), False), ((N * 3,), False),
+                                        ((N, 4), False), ((N + 1, 3), False), ((N, 3, 1), False)])
+def test_unpack_scales_shape(shape, fits):
+    p = lce.Packed8(torch.zeros(N, D_IN, dtype=U8), torch.zeros(shape, dtype=U8), T)
+    with pytest.raises(ValueError, match="GPU" if fits else "scales"):
+        lce.unpack8(p)
