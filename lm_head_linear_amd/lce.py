@@ -732,20 +732,28 @@ def linear(x, weight, bias=None, residual=None, activation="none", want_preact=F
     return LinearResult(out, preact)
 
 
+def _same_type(packed: Packed8, d_out, read: bool):
+    if read and packed.dtype != d_out.dtype:
+        raise ValueError("a checkpoint has to come from d_out's type")
+
+
 def linear_backward(d_out, x, weight, preact=None, activation="none", want_x=True,
                     want_weight=True, want_bias=False, weight_grad_dtype=None, d_weight=None,
                     d_bias=None, accumulate=False, workspace=None) -> LinearGrads:
     """Gradients of linear(): allocate those wanted (d_weight in
     weight_grad_dtype, fp32 unless given, d_bias in fp32) and (if needed) the
-    workspace, call lce_linear_backward.  x and preact may each be a Packed8;
+    workspace, call lce_linear_backward.  x and preact may each be a Packed8
+    of d_out's type (ValueError otherwise);
     x may be None without want_weight, weight without want_x.  d_weight
     [d_out][d_in] and d_bias [d_out] may be given, and are added to with
     accumulate.  What is read or written has to have its shape, preact
     d_out's (ValueError)."""
     xs = zs = None
     if isinstance(x, Packed8):
+        _same_type(x, d_out, want_weight)
         x, xs = x.codes, x.scales
     if isinstance(preact, Packed8):
+        _same_type(preact, d_out, activation != "none")
         preact, zs = preact.codes, preact.scales
     st, d_x, d_weight, d_bias = _torch_calls().linear_backward(
         d_out, x, xs, weight, preact, zs, ACTIVATIONS.get(activation, -1), want_x, want_weight,

@@ -108,3 +108,22 @@ def test_unpack_scales_shape(shape, fits):
     p = lce.Packed8(torch.zeros(N, D_IN, dtype=U8), torch.zeros(shape, dtype=U8), T)
     with pytest.raises(ValueError, match="GPU" if fits else "scales"):
         lce.unpack8(p)
+
+
+def test_backward_of_a_checkpoint_of_another_type():
+    """A checkpoint of the other 16-bit type would be rounded and saturated to
+    d_out's; the unpacked tensor of that type is refused, so it is too."""
+    other = torch.float16
+    x8 = lce.Packed8(torch.zeros(N, D_IN, dtype=U8), torch.zeros(N, 3, dtype=U8), other)
+    z8 = lce.Packed8(torch.zeros(N, D_OUT, dtype=U8), torch.zeros(N, 2, dtype=U8), other)
+    for kw in ({"x": x8}, {"preact": z8}, {"x": x8, "preact": z8, "activation": "relu"},
+               {"d_out": torch.zeros(N, D_OUT, dtype=other), "weight": torch.zeros(D_OUT, D_IN, dtype=other)}):
+        with pytest.raises(ValueError, match="checkpoint"):
+            _backward(**kw)
+    # not read: neither type matters
+    for kw in ({"x": x8, "want_weight": False}, {"preact": z8, "activation": "none"}):
+        with pytest.raises(ValueError, match="GPU"):
+            _backward(**kw)
+    with pytest.raises(ValueError, match="GPU"):
+        _backward(x=x8, preact=z8, d_out=torch.zeros(N, D_OUT, dtype=other),
+                  weight=torch.zeros(D_OUT, D_IN, dtype=other))
