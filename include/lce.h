@@ -452,7 +452,8 @@ int32_t lce_linear(const lce_tensor *x, const lce_tensor *weight, const lce_tens
  *              data == NULL (not all three)
  *   accumulate nonzero: d_weight and d_bias are added to, else overwritten
  *   workspace  LCE_U8, numel >= lce_linear_backward_workspace_bytes(...)
- * g is rounded to the 16-bit type once for the products (not for d_bias).
+ * g is rounded to the 16-bit type once for the products (not for d_bias,
+ * which adds 64 tokens in fp32 and those sums in fp64).
  * Outputs must not overlap inputs.  Only enqueues on `stream`. */
 int32_t lce_linear_backward(const lce_tensor *d_out_grad, const lce_tensor *x,
                             const lce_tensor *x_scales, const lce_tensor *weight,

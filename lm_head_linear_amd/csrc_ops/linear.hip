@@ -9,7 +9,8 @@
 //   d_weight  dW[o][i]  : m = i (X, MN-major), c = o (G, MN-major), depth n
 //                         (small tiles: X^T and G^T copies, K-major)
 // with G = dY * act'(Z), rounded to the 16-bit type once (it feeds matrix
-// instructions); the bias gradient sums the unrounded G in fp32.
+// instructions); the bias gradient sums the unrounded G, 64 tokens in fp32 and
+// those sums in fp64.
 //
 // Up to 64 tokens run in few_tokens_kernel, which is bound by the read of W;
 // more run on tiles in LDS: the 256 x 256 core of the losses where its tiles
@@ -321,8 +322,9 @@ __global__ void __launch_bounds__(256) copies_kernel(CopyJobs jobs) {
   }
 }
 
-// Adds the bias gradient's 64-row sums: 64 columns a block, a quarter of the
-// rows a wave, each in order.
+// Adds the bias gradient's 64-row sums in fp64, as every sum over tokens (fp32
+// drops what is below 2^-24 of the sum so far, and there may be 2^18 of them):
+// 64 columns a block, a quarter of the rows a wave, each in order.
 struct BiasGrad {
   const float *sums;       // [parts][d]
   int64_t parts, d;
@@ -330,13 +332,13 @@ struct BiasGrad {
   int32_t out_f32, add;
 };
 template <bool F16>
-__device__ inline void bias_grad_block(const BiasGrad &a, uint32_t bid, float *s_sum) {
+__device__ inline void bias_grad_block(const BiasGrad &a, uint32_t bid, double *s_sum) {
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int64_t col = int64_t(bid) * 64 + lane;
   const int64_t per = (a.parts + 3) / 4, begin = wave * per;
   const int64_t end = begin + per < a.parts ? begin + per : a.parts;
   if (wave < 4) {
-    float s = 0.0f;
+    double s = 0.0;
     if (col < a.d) {
 #pragma unroll 8
       for (int64_t i = begin; i < end; ++i) s += a.sums[i * a.d + col];
@@ -345,7 +347,7 @@ __device__ inline void bias_grad_block(const BiasGrad &a, uint32_t bid, float *s
   }
   __syncthreads();
   if (wave != 0 || col >= a.d) return;
-  const float s = ((s_sum[lane] + s_sum[64 + lane]) + s_sum[128 + lane]) + s_sum[192 + lane];
+  const float s = float(((s_sum[lane] + s_sum[64 + lane]) + s_sum[128 + lane]) + s_sum[192 + lane]);
   if (a.out_f32) {
     float *o = static_cast<float *>(a.out) + col;
     *o = a.add ? *o + s : s;
@@ -356,7 +358,7 @@ __device__ inline void bias_grad_block(const BiasGrad &a, uint32_t bid, float *s
 }
 template <bool F16>
 __global__ void __launch_bounds__(256) bias_grad_kernel(BiasGrad a) {
-  __shared__ float s_sum[256];
+  __shared__ double s_sum[256];
   bias_grad_block<F16>(a, blockIdx.x, s_sum);
 }
 
@@ -378,7 +380,7 @@ __global__ void __launch_bounds__(T::NT) backward_kernel(TileParams g0, OutEpi<T
     tile_block<T>(g1, e1, xcd_order(b, g1.blocks), smem);
     return;
   }
-  bias_grad_block<T::F16>(bias, b - g1.blocks, reinterpret_cast<float *>(smem));
+  bias_grad_block<T::F16>(bias, b - g1.blocks, reinterpret_cast<double *>(smem));
 }
 
 // The large backward in one launch: d_weight's tiles (operands as they lie),
@@ -398,7 +400,7 @@ __global__ void __launch_bounds__(TraitsH16W8<F16>::NT) big_backward_kernel(
   else if (b - blocks_w < blocks_x)
     big_block<CFG, TR, true, true, OutEpi<TR>>(gx, ex, b - blocks_w, blocks_x, smem);
   else
-    bias_grad_block<F16>(bias, b - blocks_w - blocks_x, reinterpret_cast<float *>(smem));
+    bias_grad_block<F16>(bias, b - blocks_w - blocks_x, reinterpret_cast<double *>(smem));
 }
 
 // Adds the K-splits ([split][cols][ld] fp32) of one or two products in order
