@@ -422,6 +422,7 @@ int64_t lce_linear_backward_workspace_bytes(int64_t n_tok, int64_t d_in, int64_t
  *   weight   [d_out*d_in] same dtype, row-major [d_out][d_in]
  *   bias     [d_out] x's dtype or LCE_F32, or data == NULL
  *   residual [n_tok*d_out] x's dtype, or data == NULL; may be out itself
+ *            (where out has x's dtype, too)
  *   activation LCE_ACT_* (else 588)
  *   preact   [n_tok*d_out] x's dtype, receives z for the backward, or
  *            data == NULL
@@ -455,7 +456,9 @@ int32_t lce_linear(const lce_tensor *x, const lce_tensor *weight, const lce_tens
  *   accumulate nonzero: d_weight and d_bias are added to, else overwritten
  *   workspace  LCE_U8, numel >= lce_linear_backward_workspace_bytes(...)
  * g is rounded to the 16-bit type once for the products (not for d_bias,
- * which adds 64 tokens in fp32 and those sums in fp64).
+ * which adds 64 tokens in fp32 and those sums in fp64): d_x and d_weight then
+ * err by about sqrt 2 times their own rounding, and a g beyond the type's range
+ * (a slope is at most 1.13) becomes infinite.
  * Outputs must not overlap inputs.  Only enqueues on `stream`. */
 int32_t lce_linear_backward(const lce_tensor *d_out_grad, const lce_tensor *x,
                             const lce_tensor *x_scales, const lce_tensor *weight,

@@ -18,11 +18,12 @@
 // where there are few (plan_product).
 //
 // Measured (bf16, one box, us a call; a library product alone takes 212):
-// 8192 x 4096 -> 4096 with bias, gelu, residual and pre-activation 255, 1.08
-// PFLOP/s: bound by the matrix cores (2 rounds of 64 steps of 1.59 us) and the
-// epilogue's 201 MB, which all compute units move at the same time; its
-// backward from 8-bit checkpoints 511 (traced: copies 79, products 489, medians
-// of calls with gaps between them, which run slower than calls in a row).
+// 8192 x 4096 -> 4096 with bias, gelu, residual and pre-activation 259, 1.06
+// PFLOP/s (255 to 266 from box to box): bound by the matrix cores (2 rounds of
+// 64 steps of 1.59 us) and the epilogue's 201 MB, which all compute units move
+// at the same time; its backward from 8-bit checkpoints 525 (511 to 531;
+// traced: copies 81, products 509, medians of calls with gaps between them,
+// which run slower than calls in a row).
 #include <math.h>
 
 #include <numeric>
@@ -160,7 +161,7 @@ __global__ void __launch_bounds__(512) few_tokens_kernel(const uint16_t *x, cons
 // to ld) and / or the padded transposed one, multiplying by the activation's
 // slope and summing columns on the way where asked.
 // Bound by memory and by the arithmetic of gelu's slope together: 8192 x 4096
-// from 8-bit checkpoints with W's transposed copy, 337 MB, 79 us (4.3 TB/s; 74
+// from 8-bit checkpoints with W's transposed copy, 337 MB, 81 us (4.2 TB/s; 73
 // at best); one job after the other 92, and 64 x 256 tiles 96.
 struct CopyJob {
   const void *src;          // [rows][cols], 16-bit, or e4m3 codes with scales
@@ -756,6 +757,13 @@ static int32_t plan_linear(int64_t n, int64_t d_in, int64_t d_out, int32_t dtype
   if (!half_type(dtype)) return LCE_DTYPE_MISMATCH;
   Layout l;
   p->product = plan_product(d_out, n, d_in, true);
+  // Odd rows of up to 64 tokens stream, whatever the layer's size.  That is the
+  // faster side for small layers (1003 -> 1531: 6.9, 8.5, 10.8, 16.1 us with 1,
+  // 16, 32, 64 tokens, tiles that read the rows as they lie 13.2, 12.6, 12.9,
+  // 12.1; 515 -> 777: 6.8 to 9.0 against 8.7 to 10.1) and not for large ones,
+  // weights not in a cache: 1003 -> 151936 105, 168, 254, 441 against 76, 78,
+  // 82, 108, 4097 -> 4097 18, 40, 64, 113 against 21, 23, 24, 27.  Padded copies
+  // take longer than those tiles everywhere.
   if (n <= kFewTokens && d_in % 8 != 0) p->product = ProductPlan{kFew};
   if (p->product.core == kFew) return LCE_OK;
   if (p->product.core == k256x256 ? d_in % 64 != 0 : d_in % 8 != 0) {
