@@ -432,7 +432,7 @@ int64_t lce_linear_backward_workspace_bytes(int64_t n_tok, int64_t d_in, int64_t
  * Products are summed in fp32; bias, activation and residual are applied to
  * the fp32 sum, and out and preact are each rounded once.  gelu and silu are
  * within (21 + 1.2 z^2) 2^-24 and (6 + 1.3 |z|) 2^-24 of their own value, small
- * results of a negative z included.  The sums run in a
+ * results of a negative z included (down to 2^-118).  The sums run in a
  * fixed order: the same call gives the same bits.  out (but for residual)
  * and preact must not overlap another buffer.  Only enqueues on `stream`.
  * Statuses as the workspace query, 582 for a short buffer. */
